@@ -48,6 +48,10 @@ class lsa_decode(ctypes.Structure):
                 ("K_shared", vp), ("V_shared", vp), ("shared_len", i64)]
 
 
+class lsa_kv8(ctypes.Structure):
+    _fields_ = [("fmt", i32), ("hkv", i32), ("page", i32), ("n_pages", i64), ("K", vp), ("V", vp), ("scale", vp)]
+
+
 class LSAError(RuntimeError):
     def __init__(self, status: int, msg: str):
         super().__init__(f"{STATUS_NAMES.get(status, status)}: {msg}")
@@ -121,6 +125,14 @@ def lib():
         L.lsa_sparse_attn_partial.argtypes = [vp, vp, vp, vp, i64, i32, i32, i32, i64, i64, vp, vp, vp]
         L.lsa_lse_combine.argtypes = [vp, vp, i32, i64, i32, vp, vp]
         L.lsa_attn_backward.argtypes = [vp, vp, vp, vp, vp, vp, i64, i32, i32, i32, i64, vp, vp, vp, vp]
+        L.lsa_kv8_write.argtypes = [P(lsa_kv8), vp, i64, vp, i64, i64, vp, vp, vp, i32, i32, vp]
+        L.lsa_kv8_attn_workspace_bytes.argtypes = [i64, i32, i32, i32]
+        L.lsa_kv8_attn_workspace_bytes.restype = sz
+        L.lsa_kv8_attn.argtypes = [P(lsa_kv8), vp, i64, i64, i32, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, sz, vp]
+        L.lsa_kv8_sparse_attn_workspace_bytes.argtypes = [i64, i32, i32]
+        L.lsa_kv8_sparse_attn_workspace_bytes.restype = sz
+        L.lsa_kv8_sparse_attn.argtypes = [P(lsa_kv8), vp, i64, i64, i32, vp, vp, vp, i32, i32, vp, i32, vp, vp, vp, sz, vp]
+        L.lsa_kv8_copy_pages.argtypes = [P(lsa_kv8), vp, vp, i64, vp]
         for name in exported_names():
             if getattr(L, name).restype is ctypes.c_int:
                 getattr(L, name).restype = i32

@@ -9,6 +9,7 @@ from __future__ import annotations
 import ctypes
 from dataclasses import dataclass, fields
 
+import numpy as np
 import torch
 
 from . import _lib
@@ -547,6 +548,220 @@ def lse_combine(O_parts, lse_parts, O=None, stream=None) -> torch.Tensor:
     check(lib().lsa_lse_combine(_ptr(O_parts), _ptr(lse_parts), world, nq, hq, _ptr(O), _stream(stream)),
           "lsa_lse_combine")
     return O
+
+
+# ------------------------------------------------ paged 8-bit K/V cache
+
+KV8_DTYPES = {"e4m3": torch.float8_e4m3fn, "int8": torch.int8}
+KV8_PAGES = (16, 32, 64, 128, 256)
+
+
+class KV8:
+    """Device arrays of one layer's paged 8-bit K/V cache (lsa_kv8): codes K
+    and V [n_pages, hkv, page, 128] (torch.float8_e4m3fn or torch.int8) and
+    their scales, fp32 [n_pages, hkv, 2], powers of two."""
+
+    def __init__(self, n_pages: int, hkv: int, page: int = 64, fmt: str = "e4m3", device="cuda"):
+        if fmt not in KV8_DTYPES:
+            raise ValueError(f"fmt: expected one of {tuple(KV8_DTYPES)}, got {fmt!r}")
+        if page not in KV8_PAGES:
+            raise ValueError(f"page: expected one of {KV8_PAGES}, got {page}")
+        if n_pages < 1 or hkv < 1:
+            raise ValueError("n_pages and hkv must be positive")
+        shape = (n_pages, hkv, page, 128)
+        K, V = (torch.zeros(shape, dtype=torch.uint8, device=device).view(KV8_DTYPES[fmt]) for _ in range(2))
+        self._wrap(K, V, torch.full((n_pages, hkv, 2), 2.0 ** -100, dtype=F32, device=device))
+
+    @classmethod
+    def of(cls, K: torch.Tensor, V: torch.Tensor, scale: torch.Tensor) -> "KV8":
+        """A cache over arrays the caller holds."""
+        if K.dtype not in KV8_DTYPES.values():
+            raise TypeError(f"K: expected one of {tuple(KV8_DTYPES.values())}, got {K.dtype}")
+        _spec(K, "K", K.dtype, (None, None, None, 128))
+        _spec(V, "V", K.dtype, tuple(K.shape))
+        _spec(scale, "scale", F32, (K.shape[0], K.shape[1], 2))
+        if K.shape[2] not in KV8_PAGES:
+            raise ValueError(f"page: expected one of {KV8_PAGES}, got {K.shape[2]}")
+        _need_cuda(K, V, scale)
+        kv = cls.__new__(cls)
+        kv._wrap(K, V, scale)
+        return kv
+
+    def _wrap(self, K, V, scale):
+        self.K, self.V, self.scale = K, V, scale
+        self.n_pages, self.hkv, self.page = int(K.shape[0]), int(K.shape[1]), int(K.shape[2])
+        self.fmt = "e4m3" if K.dtype == torch.float8_e4m3fn else "int8"
+        self.device = K.device
+        self.c = _lib.lsa_kv8(0 if self.fmt == "e4m3" else 1, self.hkv, self.page, self.n_pages, K.data_ptr(),
+                              V.data_ptr(), scale.data_ptr())
+        self._ref = ctypes.byref(self.c)
+
+
+def _rows(t, name, heads):
+    """Elements between the token rows of a bf16 [n, heads, 128] tensor whose
+    rows are dense (its token stride may be larger: a slice of a fused
+    projection)."""
+    _spec(t, name, BF16, (None, heads, 128))
+    if not t.is_cuda:
+        raise ValueError("LSA calls take CUDA tensors (there is no CPU implementation)")
+    n, dense = t.shape[0], t.shape[1] * 128
+    if n <= 1:
+        ld = dense
+        ok = t.shape[1] <= 1 or t.stride(1) == 128
+    else:
+        ld = t.stride(0)
+        ok = (t.shape[1] <= 1 or t.stride(1) == 128) and ld >= dense and ld % 8 == 0
+    if not ok or t.stride(2) != 1:
+        raise ValueError(f"{name}: token rows must be dense and a multiple of 8 elements apart, got strides {t.stride()}")
+    return ld
+
+
+def _on(dev, *ts):
+    for t in ts:
+        if t is not None and t.device != dev:
+            raise ValueError(f"LSA calls take tensors of one device: got {t.device} beside {dev}")
+
+
+class _KV8Call:
+    """The device and stream of one call: makes the cache's device current
+    while it launches, and keeps what the call allocated from reuse until
+    `stream` is done with it."""
+
+    def __init__(self, dev, stream):
+        self.dev, self.given, self.prev = dev, stream, None
+
+    def __enter__(self):
+        if torch.cuda.current_device() != self.dev.index:
+            self.prev = torch.cuda.device(self.dev)
+            self.prev.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self.prev is not None:
+            self.prev.__exit__(*exc)
+        return False
+
+    def new(self, shape, dtype):
+        t = torch.empty(shape, dtype=dtype, device=self.dev)
+        if self.given is not None:
+            t.record_stream(self.given)
+        return t
+
+    def stream(self):
+        s = self.given if self.given is not None else torch.cuda.current_stream(self.dev)
+        return ctypes.c_void_p(s.cuda_stream)
+
+
+def _table(kv, table, per_seq, name):
+    _spec(table, "table", I32, (None, None))
+    _spec(per_seq, name, I32, (table.shape[0],))
+    return int(table.shape[0]), int(table.shape[1])
+
+
+def kv8_write(kv: KV8, K: torch.Tensor, V: torch.Tensor, table: torch.Tensor, start: torch.Tensor, cu=None,
+              stream=None) -> KV8:
+    """lsa_kv8_write: new tokens' K/V rows [n, hkv, 128] bf16 into the pages of
+    their sequences: sequence b's rows cu[b] .. cu[b + 1] - 1 (cu None: one
+    token each) at positions start[b] on, in pages table[b]."""
+    n_seq, max_pages = _table(kv, table, start, "start")
+    ldk, ldv = _rows(K, "K", kv.hkv), _rows(V, "V", kv.hkv)
+    n = int(K.shape[0])
+    _spec(V, "V", BF16, tuple(K.shape))
+    _spec(cu, "cu", I32, (n_seq + 1,))
+    if cu is None and n != n_seq:
+        raise ValueError(f"K: without cu, expected one row for each of {n_seq} sequences, got {n}")
+    _need_cuda(table, start, cu)
+    _on(kv.device, K, V, table, start, cu)
+    with _KV8Call(kv.device, stream) as call:
+        check(lib().lsa_kv8_write(kv._ref, _ptr(K), ldk, _ptr(V), ldv, n, _ptr(cu), _ptr(start), _ptr(table), n_seq,
+                                  max_pages, call.stream()), "lsa_kv8_write")
+    return kv
+
+
+def kv8_attn_workspace_bytes(nq: int, n_seq: int, hq: int, hkv: int) -> int:
+    return int(lib().lsa_kv8_attn_workspace_bytes(nq, n_seq, hq, hkv))
+
+
+def kv8_sparse_attn_workspace_bytes(nq: int, hq: int, hkv: int) -> int:
+    return int(lib().lsa_kv8_sparse_attn_workspace_bytes(nq, hq, hkv))
+
+
+def _kv8_out(call, Q, O, lse, ws, need):
+    nq, hq = int(Q.shape[0]), int(Q.shape[1])
+    if O is None:
+        O = call.new((nq, hq, 128), BF16)
+    if lse is None:
+        lse = call.new((nq, hq), F32)
+    if ws is None or ws.numel() < need:
+        ws = call.new((max(need, 1),), torch.uint8)
+    return O, lse, ws
+
+
+def kv8_attn(Q: torch.Tensor, kv: KV8, table: torch.Tensor, lens: torch.Tensor, cu=None, sinks: int = 0,
+             window: int = 0, O=None, lse=None, ws=None, stream=None):
+    """lsa_kv8_attn: attention of each sequence's newest tokens over the whole
+    sequence (window > 0: over the last `window` positions and the first
+    `sinks`).  Q [nq, hq, 128] bf16, sequence b's rows cu[b] .. cu[b + 1] - 1
+    (cu None: one each); lens counts the new tokens too.  Returns (O bf16
+    [nq, hq, 128], lse fp32 [nq, hq], base 2)."""
+    n_seq, max_pages = _table(kv, table, lens, "lens")
+    ld = _rows(Q, "Q", None)
+    nq, hq = int(Q.shape[0]), int(Q.shape[1])
+    _spec(cu, "cu", I32, (n_seq + 1,))
+    _spec(O, "O", BF16, (nq, hq, 128))
+    _spec(lse, "lse", F32, (nq, hq))
+    _spec(ws, "ws", torch.uint8, (None,))
+    if cu is None and nq != n_seq:
+        raise ValueError(f"Q: without cu, expected one row for each of {n_seq} sequences, got {nq}")
+    _need_cuda(table, lens, cu, O, lse, ws)
+    _on(kv.device, Q, table, lens, cu, O, lse, ws)
+    with _KV8Call(kv.device, stream) as call:
+        O, lse, ws = _kv8_out(call, Q, O, lse, ws, kv8_attn_workspace_bytes(nq, n_seq, hq, kv.hkv))
+        check(lib().lsa_kv8_attn(kv._ref, _ptr(Q), ld, nq, hq, _ptr(cu), _ptr(table), _ptr(lens), n_seq, max_pages,
+                                 sinks, window, _ptr(O), _ptr(lse), _ptr(ws), ws.numel(), call.stream()),
+              "lsa_kv8_attn")
+    return O, lse
+
+
+def kv8_sparse_attn(Q: torch.Tensor, kv: KV8, table: torch.Tensor, lens: torch.Tensor, idx: torch.Tensor, seq=None,
+                    O=None, lse=None, ws=None, stream=None):
+    """lsa_kv8_sparse_attn: attention over index lists (the rows of `select`):
+    idx [nq, hkv, n_idx] int32 positions in the query's sequence seq[i] (seq
+    None: query i is sequence i's), -1 = padding.  Returns (O bf16
+    [nq, hq, 128], lse fp32 [nq, hq], base 2)."""
+    n_seq, max_pages = _table(kv, table, lens, "lens")
+    ld = _rows(Q, "Q", None)
+    nq, hq = int(Q.shape[0]), int(Q.shape[1])
+    _spec(idx, "idx", I32, (nq, kv.hkv, None))
+    _spec(seq, "seq", I32, (nq,))
+    _spec(O, "O", BF16, (nq, hq, 128))
+    _spec(lse, "lse", F32, (nq, hq))
+    _spec(ws, "ws", torch.uint8, (None,))
+    if seq is None and nq != n_seq:
+        raise ValueError(f"Q: without seq, expected one row for each of {n_seq} sequences, got {nq}")
+    _need_cuda(table, lens, idx, seq, O, lse, ws)
+    _on(kv.device, Q, table, lens, idx, seq, O, lse, ws)
+    with _KV8Call(kv.device, stream) as call:
+        O, lse, ws = _kv8_out(call, Q, O, lse, ws, kv8_sparse_attn_workspace_bytes(nq, hq, kv.hkv))
+        check(lib().lsa_kv8_sparse_attn(kv._ref, _ptr(Q), ld, nq, hq, _ptr(seq), _ptr(table), _ptr(lens), n_seq,
+                                        max_pages, _ptr(idx), idx.shape[2], _ptr(O), _ptr(lse), _ptr(ws), ws.numel(),
+                                        call.stream()), "lsa_kv8_sparse_attn")
+    return O, lse
+
+
+def kv8_copy_pages(kv: KV8, src, dst, stream=None) -> KV8:
+    """lsa_kv8_copy_pages: page src[i] onto page dst[i] (host sequences of page
+    numbers; no page may be written twice, or both read and written)."""
+    src, dst = (np.ascontiguousarray(x, dtype=np.int64) for x in (src, dst))
+    if src.ndim != 1 or src.shape != dst.shape:
+        raise ValueError(f"src and dst: expected two lists of one length, got shapes {src.shape} and {dst.shape}")
+    if src.size and max(src.max(), dst.max()) >= kv.n_pages or src.size and min(src.min(), dst.min()) < 0:
+        raise ValueError(f"src and dst: page numbers must be in [0, {kv.n_pages})")
+    src, dst = src.astype(np.int32), dst.astype(np.int32)
+    with _KV8Call(kv.device, stream) as call:
+        check(lib().lsa_kv8_copy_pages(kv._ref, src.ctypes.data_as(ctypes.c_void_p), dst.ctypes.data_as(ctypes.c_void_p),
+                                       src.size, call.stream()), "lsa_kv8_copy_pages")
+    return kv
 
 
 class KernelTimer:

@@ -250,7 +250,9 @@ lsa_status lsa_check_device_error(void) {
     const char* what = v == kErrWardInfeasible ? "Ward: no eligible merge left"
                      : v == kErrSelectOverflow ? "select: candidate list overflow"
                      : v == kErrIndexRange ? "attention: index entry >= T"
-                     : v == kErrTcTimeout  ? "tensor-core pipeline wait timed out" : "unknown";
+                     : v == kErrTcTimeout  ? "tensor-core pipeline wait timed out"
+                     : v == kErrKv8Page    ? "8-bit cache: page number outside the pool"
+                     : v == kErrKv8Range   ? "8-bit cache: token range outside the call or the table" : "unknown";
     return set_error(LSA_EDEVICE, "device error %d: %s", v, what);
 }
 

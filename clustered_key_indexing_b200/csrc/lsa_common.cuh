@@ -33,6 +33,8 @@ enum DeviceError : int {
     kErrSelectOverflow = 2,   // candidate list exceeded its capacity
     kErrIndexRange = 3,       // an index list entry was >= T
     kErrTcTimeout = 4,        // a tensor-core pipeline wait ran out (mbarrier never completed)
+    kErrKv8Page = 5,          // 8-bit cache: a page number outside the pool
+    kErrKv8Range = 6,         // 8-bit cache: a token range or sequence outside the call's arrays
 };
 
 // Rows of the flat search that took the exact fallback (diagnostics).

@@ -1,0 +1,355 @@
+// lsa_kv8.cu -- the paged 8-bit K/V cache: writing tokens into its pages and
+// copying pages [essay "《卡片柜》" (zhichai.net), ch. 8: the method stacks with
+// FP8 / INT quantisation; the bucket cache decides which keys are read, this
+// cache is what they are read from].
+//
+// A page holds `page` consecutive tokens of one sequence, per kv-head as
+// [page, 128] codes, so the codes of one (page, head) are contiguous and a
+// token's row is one 128-byte line.  Its scale is a power of two: dividing by
+// it and multiplying with it are exact, a code is the only rounding, and an
+// e4m3 code keeps its bits when the scale of an open page grows (unless the
+// value falls into the format's subnormal range).
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+#include <stdlib.h>
+
+#include "lsa_common.cuh"
+#include "lsa_mma.cuh"
+
+namespace lsa {
+
+constexpr int kKv8MinExp = -100;  // exponent of an all-zero page's scale
+
+// Exponent of the smallest power of two 2^e, e >= kKv8MinExp, with
+// amax <= 2^e * QMAX, from amax's bf16 magnitude bits (8 exponent, 7 mantissa
+// bits): QMAX = 448 = 1.75 * 2^8 (mantissa 96), 127 = 1.984375 * 2^6 (126).
+template <int FMT>
+__device__ __forceinline__ int kv8_exp(uint32_t m) {
+    const int E = (int)(m >> 7) - 127, f = (int)(m & 127u);
+    const int e = FMT == 0 ? E - 8 + (f > 96) : E - 6 + (f > 126);
+    return m == 0u || e < kKv8MinExp ? kKv8MinExp : e;
+}
+
+__device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// Four values already divided by the scale to four codes (round to nearest
+// even, saturating; NaN becomes the NaN code, or 0 in int8).
+template <int FMT>
+__device__ __forceinline__ uint32_t kv8_pack4(float a, float b, float c, float d) {
+    if constexpr (FMT == 0) {
+        uint32_t r;
+        asm("{\n .reg .b16 l, h;\n cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n"
+            " cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n mov.b32 %0, {l, h};\n}\n"
+            : "=r"(r)
+            : "f"(a), "f"(b), "f"(c), "f"(d));
+        return r;
+    } else {
+        auto q = [](float x) -> uint32_t { return (uint32_t)max(-127, min(127, __float2int_rn(x))) & 255u; };
+        return q(a) | (q(b) << 8) | (q(c) << 16) | (q(d) << 24);
+    }
+}
+
+// The values of four codes (without their scale), exact.
+template <int FMT>
+__device__ __forceinline__ void kv8_unpack4(uint32_t w, float (&x)[4]) {
+    if constexpr (FMT == 0) {
+        const uint32_t lo = e4m3x2_to_f16x2(w & 0xFFFFu), hi = e4m3x2_to_f16x2(w >> 16);
+        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+        x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = (float)(int8_t)(w >> (8 * i));
+    }
+}
+
+struct Kv8WriteArgs {
+    const uint16_t* K;       // new rows [n_tokens, hkv, 128], token rows k_stride / v_stride elements apart
+    const uint16_t* V;
+    int64_t k_stride, v_stride;
+    uint8_t* Kp;             // codes [n_pages, hkv, page, 128]
+    uint8_t* Vp;
+    float* scale;            // [n_pages, hkv, 2]
+    const int32_t* cu;       // [n_seq + 1], NULL: one token per sequence
+    const int32_t* start;    // [n_seq]
+    const int32_t* table;    // [n_seq, max_pages]
+    int64_t n_tokens, n_pages;
+    int32_t n_seq, max_pages, hkv;
+};
+
+// New tokens of sequence b: rows [q0, q0 + n) of the call, at positions
+// [start, start + n).  A range that does not fit the call or the table is
+// reported and counts as empty.
+__device__ __forceinline__ void kv8_new_tokens(const Kv8WriteArgs& a, int b, int page, int64_t& q0, int64_t& n,
+                                               int64_t& s0) {
+    q0 = a.cu ? a.cu[b] : b;
+    n = a.cu ? (int64_t)a.cu[b + 1] - q0 : 1;
+    s0 = a.start[b];
+    if (n == 0) return;
+    if (q0 < 0 || n < 0 || q0 + n > a.n_tokens || s0 < 0 || s0 + n > (int64_t)a.max_pages * page) {
+        raise_device_error(kErrKv8Range);
+        n = 0;
+    }
+}
+
+// One CTA per (page the call touches, kv-head, K or V): the page's new rows
+// are held in registers (16 rows a pass, 16 lanes of 16 bytes a row) between
+// the pass that finds their largest magnitude and the one that writes their
+// codes, so HBM sees each input once and each code once.  blockIdx.x counts
+// the touched pages of all sequences; every CTA finds its own by a scan over
+// the sequences' page counts.
+template <int FMT, int PASSES>
+__global__ void __launch_bounds__(256) kv8_write_kernel(Kv8WriteArgs a) {
+    constexpr int page = 16 * PASSES;
+    __shared__ int64_t s_at[4];       // first new row's position, one past the last, first row of the call, page index
+    __shared__ int32_t s_seq;
+    __shared__ uint32_t s_max[8];
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    if (wid == 0) {
+        if (a.cu == nullptr) {  // one token per sequence: touched page number b is sequence b's
+            if (lane == 0) {
+                int64_t q0, n, s0;
+                kv8_new_tokens(a, (int)blockIdx.x, page, q0, n, s0);
+                s_seq = n > 0 ? (int32_t)blockIdx.x : -1;
+                s_at[0] = s0; s_at[1] = s0 + n; s_at[2] = q0; s_at[3] = s0 / page;
+            }
+        } else {
+            if (lane == 0) s_seq = -1;
+            __syncwarp();
+            int64_t base = 0;
+            for (int b0 = 0; b0 < a.n_seq && base <= (int64_t)blockIdx.x; b0 += 32) {
+                const int b = b0 + lane;
+                int64_t q0 = 0, n = 0, s0 = 0, m = 0;
+                if (b < a.n_seq) kv8_new_tokens(a, b, page, q0, n, s0);
+                if (n > 0) m = (s0 + n - 1) / page - s0 / page + 1;
+                int64_t inc = m;
+#pragma unroll
+                for (int off = 1; off < 32; off <<= 1) {
+                    const int64_t up = __shfl_up_sync(0xffffffffu, inc, off);
+                    if (lane >= off) inc += up;
+                }
+                const int64_t k = (int64_t)blockIdx.x - (base + inc - m);
+                if (k >= 0 && k < m) {
+                    s_seq = b;
+                    s_at[0] = s0; s_at[1] = s0 + n; s_at[2] = q0; s_at[3] = s0 / page + k;
+                }
+                base += __shfl_sync(0xffffffffu, inc, 31);
+            }
+        }
+    }
+    __syncthreads();
+    const int seq = s_seq;
+    if (seq < 0) return;
+    const int h = blockIdx.y, kv = blockIdx.z;
+    const int64_t p0 = s_at[0], p1 = s_at[1], pg = s_at[3];
+    const int64_t pid = a.table[(int64_t)seq * a.max_pages + pg];
+    if (pid < 0 || pid >= a.n_pages) {
+        if (tid == 0) raise_device_error(kErrKv8Page);
+        return;
+    }
+    const int r0 = (int)max((int64_t)0, p0 - pg * page);                   // rows below r0 were written before
+    const int r1 = (int)min((int64_t)page, p1 - pg * page);
+    const int64_t stride = kv ? a.v_stride : a.k_stride;
+    const uint16_t* src = (kv ? a.V : a.K) + (s_at[2] + pg * page - p0) * stride + (int64_t)h * kD;  // row 0 of the page
+    uint8_t* dst = (kv ? a.Vp : a.Kp) + (pid * a.hkv + h) * (int64_t)page * kD;
+    float* sp = a.scale + (pid * a.hkv + h) * 2 + kv;
+    const int rr = tid >> 4, c = tid & 15;
+
+    uint4 x[PASSES];
+    uint32_t mx = 0u;
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+        const int r = 16 * i + rr;
+        x[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (r >= r0 && r < r1) x[i] = *reinterpret_cast<const uint4*>(src + r * stride + c * 8);
+    }
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t lo = w[j] & 0x7FFFu, hi = (w[j] >> 16) & 0x7FFFu;  // finite magnitudes order as integers
+            mx = max(mx, lo < 0x7F80u ? lo : 0u);
+            mx = max(mx, hi < 0x7F80u ? hi : 0u);
+        }
+    }
+    mx = __reduce_max_sync(0xffffffffu, mx);
+    if (lane == 0) s_max[wid] = mx;
+    const float old = r0 > 0 ? *sp : 0.f;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) mx = max(mx, s_max[i]);
+    const int e = kv8_exp<FMT>(mx);
+    const float need = pow2f(e);
+    if (r0 > 0 && need > old) {
+        // the open page's scale grows: its kept rows move to the new one
+        const float f = old * pow2f(-e);
+        for (int i = tid; i < r0 * (kD / 4); i += 256) {
+            uint32_t* p = reinterpret_cast<uint32_t*>(dst) + i;
+            float v[4];
+            kv8_unpack4<FMT>(*p, v);
+            *p = kv8_pack4<FMT>(v[0] * f, v[1] * f, v[2] * f, v[3] * f);
+        }
+    }
+    const float s = r0 > 0 ? fmaxf(need, old) : need;
+    const float inv = r0 > 0 && old >= need ? 1.0f / old : pow2f(-e);  // a power of two: exact
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+        const int r = 16 * i + rr;
+        if (r < r0 || r >= r1) continue;
+        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[2 * j] = __uint_as_float(w[j] << 16) * inv;
+            v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u) * inv;
+        }
+        *reinterpret_cast<uint2*>(dst + r * kD + c * 8) =
+            make_uint2(kv8_pack4<FMT>(v[0], v[1], v[2], v[3]), kv8_pack4<FMT>(v[4], v[5], v[6], v[7]));
+    }
+    if (tid == 0) *sp = s;
+}
+
+// Page copies.  The pairs travel in the launch's own arguments: no upload, and
+// a captured launch keeps them.  One CTA moves 16 KB of one page's K or V;
+// the first CTA of a page also moves its scales.
+template <int N>
+struct Kv8Pairs {
+    int32_t src[N], dst[N];
+};
+
+constexpr int kCopyChunk = 16384;
+
+template <int N>
+__global__ void __launch_bounds__(256) kv8_copy_kernel(const __grid_constant__ Kv8Pairs<N> p, uint8_t* K, uint8_t* V,
+                                                       float* scale, int64_t page_bytes, int32_t nchunk, int32_t hkv) {
+    const int i = blockIdx.x / nchunk, ch = blockIdx.x % nchunk;
+    uint8_t* pool = blockIdx.y ? V : K;
+    const int64_t s = p.src[i], d = p.dst[i];
+    const uint4* from = reinterpret_cast<const uint4*>(pool + s * page_bytes);
+    uint4* to = reinterpret_cast<uint4*>(pool + d * page_bytes);
+    const int64_t n = page_bytes / 16;
+    const int64_t at = (int64_t)ch * (kCopyChunk / 16) + threadIdx.x;
+    uint4 x[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+        if (at + 256 * u < n) x[u] = __ldcs(from + at + 256 * u);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+        if (at + 256 * u < n) __stcs(to + at + 256 * u, x[u]);
+    if (ch == 0 && blockIdx.y == 0)
+        for (int j = threadIdx.x; j < 2 * hkv; j += 256) scale[d * 2 * hkv + j] = scale[s * 2 * hkv + j];
+}
+
+static lsa_status check_kv8(const lsa_kv8* c) {
+    if (!c) return set_error(LSA_EINVAL, "kv8: cache is NULL");
+    if (c->fmt != LSA_KV8_E4M3 && c->fmt != LSA_KV8_INT8) return set_error(LSA_EINVAL, "kv8: fmt must be 0 (e4m3) or 1 (int8)");
+    if (c->hkv <= 0 || c->n_pages <= 0) return set_error(LSA_EINVAL, "kv8: hkv and n_pages must be positive");
+    if (c->hkv > 65535) return set_error(LSA_EUNSUPPORTED, "kv8: hkv > 65535");
+    if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128 && c->page != 256)
+        return set_error(LSA_EUNSUPPORTED, "kv8: page must be 16, 32, 64, 128 or 256 tokens");
+    if (c->n_pages > (int64_t)INT32_MAX / ((int64_t)c->hkv * c->page))
+        return set_error(LSA_EUNSUPPORTED, "kv8: more than 2^31 rows of codes");
+    if (!c->K || !c->V || !c->scale) return set_error(LSA_EINVAL, "kv8: K, V or scale is NULL");
+    if (!aligned16(c->K) || !aligned16(c->V) || ((uintptr_t)c->scale & 7u))
+        return set_error(LSA_EINVAL, "kv8: K and V must be 16-byte aligned, scale 8-byte");
+    return LSA_OK;
+}
+
+template <int FMT>
+static void launch_kv8_write(const Kv8WriteArgs& a, int page, dim3 grid, cudaStream_t st) {
+    switch (page) {
+        case 16: kv8_write_kernel<FMT, 1><<<grid, 256, 0, st>>>(a); break;
+        case 32: kv8_write_kernel<FMT, 2><<<grid, 256, 0, st>>>(a); break;
+        case 64: kv8_write_kernel<FMT, 4><<<grid, 256, 0, st>>>(a); break;
+        case 128: kv8_write_kernel<FMT, 8><<<grid, 256, 0, st>>>(a); break;
+        default: kv8_write_kernel<FMT, 16><<<grid, 256, 0, st>>>(a); break;
+    }
+}
+
+template <int N>
+static void launch_kv8_copy(const lsa_kv8* c, const int32_t* src, const int32_t* dst, int n, cudaStream_t st) {
+    Kv8Pairs<N> p;
+    for (int i = 0; i < n; ++i) { p.src[i] = src[i]; p.dst[i] = dst[i]; }
+    const int64_t bytes = (int64_t)c->hkv * c->page * kD;
+    const int nchunk = (int)ceil_div<int64_t>(bytes, kCopyChunk);
+    kv8_copy_kernel<N><<<dim3((unsigned)(n * nchunk), 2), 256, 0, st>>>(p, c->K, c->V, c->scale, bytes, nchunk, c->hkv);
+}
+
+}  // namespace lsa
+
+extern "C" {
+
+lsa_status lsa_kv8_write(const lsa_kv8* kv, const uint16_t* K, int64_t k_stride, const uint16_t* V, int64_t v_stride,
+                         int64_t n_tokens, const int32_t* cu, const int32_t* start, const int32_t* table,
+                         int32_t n_seq, int32_t max_pages, void* stream) {
+    using namespace lsa;
+    lsa_status s;
+    if ((s = check_kv8(kv)) != LSA_OK) return s;
+    if (n_tokens < 0 || n_seq < 0 || max_pages < 0) return set_error(LSA_EINVAL, "lsa_kv8_write: negative size");
+    if (!cu && n_tokens != n_seq) return set_error(LSA_EINVAL, "lsa_kv8_write: without cu, n_tokens must equal n_seq");
+    if (n_tokens == 0 || n_seq == 0) return LSA_OK;
+    if (!K || !V || !start || !table) return set_error(LSA_EINVAL, "lsa_kv8_write: NULL pointer");
+    if (k_stride < (int64_t)kv->hkv * kD || v_stride < (int64_t)kv->hkv * kD || (k_stride & 7) || (v_stride & 7))
+        return set_error(LSA_EINVAL, "lsa_kv8_write: token strides must be multiples of 8 elements, at least hkv * 128");
+    if (!aligned16(K) || !aligned16(V)) return set_error(LSA_EINVAL, "lsa_kv8_write: K and V must be 16-byte aligned");
+    // pages a sequence touches: at most n / page + 2
+    const int64_t items = cu ? n_tokens / kv->page + 2 * (int64_t)n_seq : n_seq;
+    if (n_tokens > INT32_MAX || items > INT32_MAX) return set_error(LSA_EUNSUPPORTED, "lsa_kv8_write: n_tokens beyond 2^31");
+    Kv8WriteArgs a{};
+    a.K = K; a.V = V; a.k_stride = k_stride; a.v_stride = v_stride;
+    a.Kp = kv->K; a.Vp = kv->V; a.scale = kv->scale;
+    a.cu = cu; a.start = start; a.table = table; a.n_tokens = n_tokens; a.n_pages = kv->n_pages;
+    a.n_seq = n_seq; a.max_pages = max_pages; a.hkv = kv->hkv;
+    const cudaStream_t st = (cudaStream_t)stream;
+    {
+        KTime kt_("kv8_write_kernel", st);
+        const dim3 grid((unsigned)items, (unsigned)kv->hkv, 2);
+        if (kv->fmt == LSA_KV8_E4M3) launch_kv8_write<0>(a, kv->page, grid, st);
+        else launch_kv8_write<1>(a, kv->page, grid, st);
+    }
+    return check_launch("kv8_write_kernel");
+}
+
+lsa_status lsa_kv8_copy_pages(const lsa_kv8* kv, const int32_t* src, const int32_t* dst, int64_t n, void* stream) {
+    using namespace lsa;
+    lsa_status s;
+    if ((s = check_kv8(kv)) != LSA_OK) return s;
+    if (n < 0) return set_error(LSA_EINVAL, "lsa_kv8_copy_pages: n < 0");
+    if (n == 0) return LSA_OK;
+    if (!src || !dst) return set_error(LSA_EINVAL, "lsa_kv8_copy_pages: NULL pointer");
+    if (n > kv->n_pages) return set_error(LSA_EINVAL, "lsa_kv8_copy_pages: more copies than pages");
+    for (int64_t i = 0; i < n; ++i)
+        if (src[i] < 0 || src[i] >= kv->n_pages || dst[i] < 0 || dst[i] >= kv->n_pages)
+            return set_error(LSA_EINVAL, "lsa_kv8_copy_pages: pair %lld (%d -> %d) is outside the pool's %lld pages",
+                             (long long)i, src[i], dst[i], (long long)kv->n_pages);
+    // the copies run in no order: no page may be written twice, or written and read
+    uint8_t* mark = (uint8_t*)calloc((size_t)(kv->n_pages + 7) / 8, 1);
+    if (!mark) return set_error(LSA_ENOSPACE, "lsa_kv8_copy_pages: out of host memory");
+    int64_t bad = -1;
+    for (int64_t i = 0; i < n && bad < 0; ++i) {
+        if (mark[dst[i] >> 3] & (1u << (dst[i] & 7))) bad = i;
+        mark[dst[i] >> 3] |= (uint8_t)(1u << (dst[i] & 7));
+    }
+    for (int64_t i = 0; i < n && bad < 0; ++i)
+        if (mark[src[i] >> 3] & (1u << (src[i] & 7))) bad = i;
+    free(mark);
+    if (bad >= 0)
+        return set_error(LSA_EINVAL, "lsa_kv8_copy_pages: pair %lld (%d -> %d): a page is written twice, or read and written",
+                         (long long)bad, src[bad], dst[bad]);
+    const cudaStream_t st = (cudaStream_t)stream;
+    constexpr int kFew = 60, kMany = 2000;  // 480 bytes or 16 KB of arguments
+    for (int64_t i = 0; i < n; i += kMany) {
+        const int m = (int)(n - i < kMany ? n - i : kMany);
+        {
+            KTime kt_("kv8_copy_kernel", st);
+            if (m <= kFew) launch_kv8_copy<kFew>(kv, src + i, dst + i, m, st);
+            else launch_kv8_copy<kMany>(kv, src + i, dst + i, m, st);
+        }
+        if ((s = check_launch("kv8_copy_kernel")) != LSA_OK) return s;
+    }
+    return LSA_OK;
+}
+
+}  // extern "C"

@@ -588,6 +588,110 @@ lsa_status lsa_sparse_attn_partial(const uint16_t* Q, const uint16_t* K, const u
 lsa_status lsa_lse_combine(const float* O_parts, const float* lse_parts, int32_t world, int64_t nq,
                            int32_t hq, uint16_t* O, void* stream);
 
+/* ------------------------------------------------- paged 8-bit K/V cache */
+
+/*
+ * K/V of one layer in 8 bits, in pages that sequences own through a table
+ * [essay ch. 8: the method stacks with 8-bit quantisation; the pages give no
+ * layout].  Page p holds `page` consecutive tokens of one sequence:
+ *   K, V   [n_pages, hkv, page, d_head] codes: OCP e4m3 (fmt LSA_KV8_E4M3) or
+ *          two's complement int8 in -127 .. 127 (LSA_KV8_INT8);
+ *   scale  [n_pages, hkv, 2] fp32, K's and V's: powers of two 2^e with
+ *          -100 <= e <= 120.  A code's value is code * scale.
+ * Token t of sequence b is row t % page of page table[b, t / page]; `table`
+ * is int32 [n_seq, max_pages] on the device, entries behind a sequence's last
+ * page are not read.  Sequences may share pages (a forked prefix): reading
+ * them is always allowed, lsa_kv8_write must be given pages of its own.
+ * A page number outside the pool, or a token range outside the table, raises
+ * the device error word (LSA_EDEVICE at the next lsa_check_device_error) and
+ * the rows concerned are skipped.  page is 16, 32, 64, 128 or 256; n_pages *
+ * hkv * page < 2^31; K and V 16-byte aligned, scale 8-byte.
+ */
+#define LSA_KV8_E4M3 0
+#define LSA_KV8_INT8 1
+typedef struct lsa_kv8 {
+    int32_t  fmt;       /* LSA_KV8_E4M3 or LSA_KV8_INT8 */
+    int32_t  hkv;
+    int32_t  page;      /* tokens per page              */
+    int64_t  n_pages;
+    uint8_t* K;
+    uint8_t* V;
+    float*   scale;
+} lsa_kv8;
+
+/*
+ * lsa_kv8_write -- write new tokens' K/V rows into their pages.  K, V
+ * [n_tokens, hkv, d_head] bf16, 16-byte aligned, token rows k_stride /
+ * v_stride elements apart (multiples of 8, at least hkv * d_head).  Sequence b
+ * gets rows cu[b] .. cu[b + 1] - 1 (cu NULL: one token each, n_tokens ==
+ * n_seq) at positions start[b] on; cu [n_seq + 1] and start [n_seq] are int32
+ * on the device.
+ * Per page, kv-head and tensor, with QMAX = 448 (e4m3) or 127 (int8):
+ *   a page whose first row is written: scale = the smallest 2^e, e >= -100,
+ *     with max |x| <= 2^e QMAX over the finite new values;
+ *   a page that was open: scale = max(its scale, that power of two); if it
+ *     grew, the rows written before are rounded again at the new scale (an
+ *     e4m3 code keeps its value unless it turns subnormal);
+ *   code = x / scale rounded to nearest even, saturated (infinities too); NaN
+ *     gives the e4m3 NaN code, and 0 in int8.
+ * Rows behind the new tokens keep their bytes.  No two new tokens may share a
+ * page unless they belong to the same sequence.
+ */
+lsa_status lsa_kv8_write(const lsa_kv8* kv, const uint16_t* K, int64_t k_stride,
+                         const uint16_t* V, int64_t v_stride, int64_t n_tokens,
+                         const int32_t* cu, const int32_t* start, const int32_t* table,
+                         int32_t n_seq, int32_t max_pages, void* stream);
+
+/* Workspace bytes of lsa_kv8_attn for nq queries of n_seq sequences, and of
+ * lsa_kv8_sparse_attn for nq queries (0: none needed). */
+size_t lsa_kv8_attn_workspace_bytes(int64_t nq, int32_t n_seq, int32_t hq, int32_t hkv);
+size_t lsa_kv8_sparse_attn_workspace_bytes(int64_t nq, int32_t hq, int32_t hkv);
+
+/*
+ * lsa_kv8_attn -- exact softmax attention of the newest tokens over their
+ * whole sequences.  lens [n_seq] int32: tokens each sequence holds, the new
+ * ones included (lsa_kv8_write first).  Sequence b's queries are rows cu[b] ..
+ * cu[b + 1] - 1 of Q (cu NULL: one each, nq == n_seq), its n newest tokens in
+ * order: query i sits at t = lens[b] - n + i and attends keys j <= t, and if
+ * window > 0 only j > t - window or j < sinks.  Q [nq, hq, d_head] bf16,
+ * token rows q_stride elements apart (a multiple of 8); O [nq, hq, d_head]
+ * bf16; lse (may be NULL) [nq, hq] fp32, the base-2 log-sum-exp of the scores
+ * scaled by log2(e) / sqrt(d_head).  A row with no key gives O = 0 and lse =
+ * -inf.  Every group of 8 (16, when sequences have more than 8 on average)
+ * columns -- (new token, query head of one kv-head) pairs -- reads the cache
+ * once: made for decoded and drafted tokens, not for whole prompts.
+ * ws: lsa_kv8_attn_workspace_bytes(), 16-byte aligned; calls that may run at
+ * the same time need one each.  hq / hkv must be 1, 2, 4 or 8.
+ */
+lsa_status lsa_kv8_attn(const lsa_kv8* kv, const uint16_t* Q, int64_t q_stride, int64_t nq,
+                        int32_t hq, const int32_t* cu, const int32_t* table,
+                        const int32_t* lens, int32_t n_seq, int32_t max_pages,
+                        int32_t sinks, int32_t window, uint16_t* O, float* lse, void* ws,
+                        size_t ws_bytes, void* stream);
+
+/*
+ * lsa_kv8_sparse_attn -- lsa_sparse_attn over the cache: query i attends the
+ * entries j >= 0 of idx[i, g, 0:n_idx] (positions in its sequence; a position
+ * that stands twice counts twice), in prefill chunks and in decode.  seq [nq]
+ * int32: the sequence of each query (NULL: query i is sequence i's, nq ==
+ * n_seq).  An entry >= lens[seq] raises the device error word and is skipped.
+ * Q, O, lse and ws as lsa_kv8_attn (lsa_kv8_sparse_attn_workspace_bytes()).
+ */
+lsa_status lsa_kv8_sparse_attn(const lsa_kv8* kv, const uint16_t* Q, int64_t q_stride, int64_t nq,
+                               int32_t hq, const int32_t* seq, const int32_t* table,
+                               const int32_t* lens, int32_t n_seq, int32_t max_pages,
+                               const int32_t* idx, int32_t n_idx, uint16_t* O, float* lse,
+                               void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * lsa_kv8_copy_pages -- copy the codes and scales of page src[i] to page
+ * dst[i], i < n (forks, compaction).  src and dst are HOST arrays, read during
+ * the call.  LSA_EINVAL if a page number is outside the pool, a page is
+ * written twice, or one is both read and written.
+ */
+lsa_status lsa_kv8_copy_pages(const lsa_kv8* kv, const int32_t* src, const int32_t* dst, int64_t n,
+                              void* stream);
+
 #ifdef __cplusplus
 }
 #endif
