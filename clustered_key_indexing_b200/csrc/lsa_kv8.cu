@@ -252,8 +252,8 @@ static lsa_status check_kv8(const lsa_kv8* c) {
     if (c->n_pages > (int64_t)INT32_MAX / ((int64_t)c->hkv * c->page))
         return set_error(LSA_EUNSUPPORTED, "kv8: more than 2^31 rows of codes");
     if (!c->K || !c->V || !c->scale) return set_error(LSA_EINVAL, "kv8: K, V or scale is NULL");
-    if (!aligned16(c->K) || !aligned16(c->V) || ((uintptr_t)c->scale & 7u))
-        return set_error(LSA_EINVAL, "kv8: K and V must be 16-byte aligned, scale 8-byte");
+    if ((((uintptr_t)c->K | (uintptr_t)c->V) & 127u) || ((uintptr_t)c->scale & 7u))
+        return set_error(LSA_EINVAL, "kv8: K and V must be 128-byte aligned, scale 8-byte");
     return LSA_OK;
 }
 

@@ -6,15 +6,18 @@
 // heads of the group; of several new tokens, 8 or 16 (token, head) pairs):
 //   S^T = K Q^T   keys are the MMA's M dimension, columns its N;
 //   O^T += V^T P^T.
-// Codes go from global memory straight into registers, 16 bytes a lane, in
-// an order that makes them MMA operands without a shuffle: the K dimension of
-// S^T is a permutation of the 128 dims (lane (g, t) holds dims 16 t .. + 15
-// and 64 + 16 t .. + 15 of key rows g and g + 8, Q follows the same order),
-// and the M dimension of O^T is one too (lane (g, t) holds dims 16 g .. + 15
-// of key rows 2t, 2t+1, 2t+8, 2t+9; byte pairs of two rows are interleaved
+// Rows of codes travel through a per-warp ring in shared memory (cp.async, two
+// steps ahead; through registers instead, with one step ahead, a million
+// tokens took 667 us against 420: too few bytes in flight) and are read 16
+// bytes a lane in an order that makes them MMA operands without a shuffle: the
+// K dimension of S^T is a permutation of the 128 dims (lane (g, t) holds dims
+// 32 t .. + 31 of key rows g and g + 8, Q follows the same order), and the M
+// dimension of O^T is one too (lane (g, t) holds dims 16 g .. + 15 of key rows
+// 2t, 2t+1, 2t+8, 2t+9; byte pairs of two rows are interleaved
 // with one byte permute).  Codes become fp16 exactly; Q is divided by its
 // row's power of two and becomes fp16 (exact to 2^-17 of the row's largest
-// element, absolute error 2^-25 of it below that); P is fp16 with 12 bits of
+// element, absolute error 2^-25 of it below that; an e4m3 mma.sync converts
+// both operands to fp16 itself and was slower); P is fp16 with 12 bits of
 // headroom (an entry 2^-26 of the largest still has all its bits).  Scores,
 // softmax sums and outputs are fp32.  The K scale multiplies the scores; the
 // V scale, a power of two, multiplies P relative to the largest V scale seen
@@ -32,6 +35,7 @@
 namespace lsa {
 
 constexpr int kKv8Warps = 8;
+constexpr int kKv8ListWarps = 8;
 constexpr float kKv8Head = 12.f;   // log2 of P's headroom
 constexpr float kKv8Lazy = 2.f;    // log2 growth that moves the running maximum
 
@@ -61,8 +65,9 @@ struct Kv8AttnArgs {
 template <int FMT>
 __device__ __forceinline__ void kv8_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
     if constexpr (FMT == 0) {
-        lo = e4m3x2_to_f16x2(w & 0xFFFFu);
-        hi = e4m3x2_to_f16x2(w >> 16);
+        asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}\n"
+            : "=r"(lo), "=r"(hi)
+            : "r"(w));
     } else {
         const uint32_t u = w ^ 0x80808080u;
         const __half2 bias = __half2half2(__ushort_as_half((unsigned short)0x6480));  // 1152
@@ -86,13 +91,16 @@ __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
     return r;
 }
 
-__device__ __forceinline__ uint4 ldg_codes(const uint8_t* p, bool ok) {
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (ok) v = __ldg(reinterpret_cast<const uint4*>(p));
-    return v;
+// 2^x, subnormal results flushed (they are below 2^-126 of the largest).
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
+    return r;
 }
 
 // ------------------------------------------------------------ warp state
+
+__device__ __forceinline__ uint32_t word_of(const uint4& v, int j) { return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w; }
 
 template <int NT>
 struct Kv8State {
@@ -103,8 +111,8 @@ struct Kv8State {
     float vref;             // the V scale that O is relative to
 };
 
-// Q row of column n (gq within tile nt): 32 of its 128 dims per lane, to fp16
-// B operands in the permuted order, with its power of two.
+// Q row of each column (gq within tile nt; NULL: none), dims 32 t .. + 31 on
+// this lane, divided by the row's power of two.
 template <int NT>
 __device__ __forceinline__ void kv8_load_q(Kv8State<NT>& s, const uint16_t* const (&row)[NT], float scale_log2) {
     const int lane = threadIdx.x & 31, tq = lane & 3;
@@ -114,7 +122,7 @@ __device__ __forceinline__ void kv8_load_q(Kv8State<NT>& s, const uint16_t* cons
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             x[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (row[nt]) x[i] = __ldg(reinterpret_cast<const uint4*>(row[nt] + (i >> 1) * 64 + 16 * tq + (i & 1) * 8));
+            if (row[nt]) x[i] = __ldg(reinterpret_cast<const uint4*>(row[nt] + 32 * tq + 8 * i));
         }
         uint32_t mx = 0u;
 #pragma unroll
@@ -125,18 +133,16 @@ __device__ __forceinline__ void kv8_load_q(Kv8State<NT>& s, const uint16_t* cons
         }
         mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        // |q| < 2^(E - 126): divide by 2^e, e = E - 126 in [-120, 120]
-        const int e = mx == 0u ? 0 : max(-120, min(120, (int)(mx >> 7) - 126));
+        // |q| < 2^(E - 126): below 1 after the division by 2^e
+        const int e = mx == 0u ? 0 : max(-100, min(110, (int)(mx >> 7) - 126));
         const float inv = __uint_as_float((uint32_t)(127 - e) << 23), f = __uint_as_float((uint32_t)(127 + e) << 23) * scale_log2;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        for (int i = 0; i < 8; ++i)  // dims 32 t + 4 i .. + 3
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {  // dims (i >> 1) * 64 + 16 t + (i & 1) * 8 + 2 j, + 1: k-step (i >> 1) * 4 + (i & 1) * 2 + j / 2
-                const float a = __uint_as_float(w[j] << 16) * inv, b = __uint_as_float(w[j] & 0xFFFF0000u) * inv;
-                s.qb[nt][(i >> 1) * 4 + (i & 1) * 2 + (j >> 1)][j & 1] = pack_f16x2(a, b);
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t w = word_of(x[i >> 1], 2 * (i & 1) + h);
+                s.qb[nt][i][h] = pack_f16x2(__uint_as_float(w << 16) * inv, __uint_as_float(w & 0xFFFF0000u) * inv);
             }
-        }
         s.cf[nt][0] = __shfl_sync(0xffffffffu, f, (2 * tq) * 4);
         s.cf[nt][1] = __shfl_sync(0xffffffffu, f, (2 * tq + 1) * 4);
 #pragma unroll
@@ -149,9 +155,14 @@ __device__ __forceinline__ void kv8_load_q(Kv8State<NT>& s, const uint16_t* cons
     s.vref = 0x1p-100f;
 }
 
-// S^T of 16 keys: k[0..1] the lane's chunks of key row g, k[2..3] of row g + 8.
+// The lane's 32 codes (dims 32 t .. + 31) of key rows g and g + 8.
+struct Kv8K {
+    uint4 a[2], b[2];
+};
+
+// S^T of 16 keys.
 template <int FMT, int NT>
-__device__ __forceinline__ void kv8_scores(const Kv8State<NT>& s, const uint4 (&k)[4], float (&sc)[NT][4]) {
+__device__ __forceinline__ void kv8_scores(const Kv8State<NT>& s, const Kv8K& k, float (&sc)[NT][4]) {
     float c[NT][2][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -160,16 +171,12 @@ __device__ __forceinline__ void kv8_scores(const Kv8State<NT>& s, const uint4 (&
 #pragma unroll
             for (int i = 0; i < 4; ++i) c[nt][h][i] = 0.f;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const uint32_t wa[4] = {k[h].x, k[h].y, k[h].z, k[h].w}, wb[4] = {k[2 + h].x, k[2 + h].y, k[2 + h].z, k[2 + h].w};
+    for (int i = 0; i < 8; ++i) {
+        uint32_t a[4];
+        kv8_f16<FMT>(word_of(k.a[i >> 2], i & 3), a[0], a[2]);
+        kv8_f16<FMT>(word_of(k.b[i >> 2], i & 3), a[1], a[3]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            uint32_t a[4];
-            kv8_f16<FMT>(wa[j], a[0], a[2]);
-            kv8_f16<FMT>(wb[j], a[1], a[3]);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_16816_f16(c[nt][h], a, s.qb[nt][4 * h + j][0], s.qb[nt][4 * h + j][1]);
-        }
+        for (int nt = 0; nt < NT; ++nt) mma_16816_f16(c[nt][i & 1], a, s.qb[nt][i][0], s.qb[nt][i][1]);
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -186,8 +193,6 @@ __device__ __forceinline__ void kv8_v_operands(const uint32_t (&w)[4], uint32_t 
     kv8_f16<FMT>(__byte_perm(w[0], w[1], 0x7362), a1[0], a1[1]);
     kv8_f16<FMT>(__byte_perm(w[2], w[3], 0x7362), a1[2], a1[3]);
 }
-
-__device__ __forceinline__ uint32_t word_of(const uint4& v, int j) { return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w; }
 
 template <int FMT, int NT>
 __device__ __forceinline__ void kv8_pv(Kv8State<NT>& s, const uint4 (&v)[4], const uint32_t (&pb)[NT][2]) {
@@ -226,7 +231,7 @@ __device__ __forceinline__ void kv8_softmax(Kv8State<NT>& s, const float (&sc)[N
                 mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
             }
             const float n0 = fmaxf(s.m[nt][0], mx0), n1 = fmaxf(s.m[nt][1], mx1);
-            const float a0 = exp2f(s.m[nt][0] - n0), a1 = exp2f(s.m[nt][1] - n1);
+            const float a0 = ex2(s.m[nt][0] - n0), a1 = ex2(s.m[nt][1] - n1);
             s.m[nt][0] = n0;
             s.m[nt][1] = n1;
             s.l[nt][0] *= a0;
@@ -238,12 +243,13 @@ __device__ __forceinline__ void kv8_softmax(Kv8State<NT>& s, const float (&sc)[N
             }
         }
     }
-    const float iv = 1.0f / s.vref, w0 = vs0 * iv, w1 = vs1 * iv;
+    // 1 / vref: the reciprocal of a power of two, exactly
+    const float iv = __uint_as_float(0x7F000000u - __float_as_uint(s.vref)), w0 = vs0 * iv, w1 = vs1 * iv;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const float b0 = s.m[nt][0] - kKv8Head, b1 = s.m[nt][1] - kKv8Head;
-        const float e0 = exp2f(sc[nt][0] - b0), e1 = exp2f(sc[nt][1] - b1);
-        const float e2 = exp2f(sc[nt][2] - b0), e3 = exp2f(sc[nt][3] - b1);
+        const float e0 = ex2(sc[nt][0] - b0), e1 = ex2(sc[nt][1] - b1);
+        const float e2 = ex2(sc[nt][2] - b0), e3 = ex2(sc[nt][3] - b1);
         s.l[nt][0] += e0 + e2;
         s.l[nt][1] += e1 + e3;
         pb[nt][0] = movmatrix_t(pack_f16x2(e0 * w0, e1 * w0));
@@ -268,19 +274,53 @@ __device__ __forceinline__ uint16_t bf16_bits(float x) {
     return *reinterpret_cast<const uint16_t*>(&b);
 }
 
-// --------------------------------------------------- index lists, one row
+// ------------------------------------------------- the keys of one row
 
-// Keys [16 tile, 16 tile + 16) of a list: lanes l and l + 16 hold entry l as
-// its row of codes (-1: none) and its two scales (bf16 halves: powers of two).
-struct Kv8List {
-    const int32_t* list;   // NULL: the query's sequence number is out of range
-    const int32_t* table;  // the sequence's row
-    int32_t len, n_idx, max_pages, hkv, g, lgp;
-    int64_t n_pages;
+// A row's keys come in chunks of 32 entries, one a lane: the positions of an
+// index list, or (dense) those that the row's mask leaves, in order.
+template <bool LIST>
+struct Kv8Keys {
+    const int32_t* list;   // lists: entries (NULL: none)
+    const int32_t* table;  // the sequence's pages
+    int32_t len, n_idx, g;
+    // dense: chunks [0, n_sink) and from c_lo on; positions of the row's first
+    // and last query, first key of the first one's window
+    int32_t n_sink, c_lo, tmin, tmax, lo;
+
+    __device__ __forceinline__ int key0(int c) const { return 32 * (c < n_sink ? c : c - n_sink + c_lo); }
+
+    // Entry of this lane in chunk c, -1 for none.
+    __device__ __forceinline__ int entry(const Kv8AttnArgs& a, int c, int cend) const {
+        const int lane = threadIdx.x & 31;
+        if (c >= cend) return -1;
+        if constexpr (LIST) {
+            const int e = 32 * c + lane;
+            return list != nullptr && e < n_idx ? __ldg(list + e) : -1;
+        } else {
+            const int j = key0(c) + lane;
+            return j <= tmax && (j >= lo || j < a.S) ? j : -1;
+        }
+    }
+
+    // Row of codes of an entry, -1 for none.
+    __device__ __forceinline__ int row(const Kv8AttnArgs& a, int p) const {
+        if (p < 0) return -1;
+        const int pg = p >> a.lgp;
+        if (LIST && (p >= len || pg >= a.max_pages)) {
+            raise_device_error(kErrIndexRange);
+            return -1;
+        }
+        const int pid = __ldg(table + pg);
+        if (pid < 0 || pid >= a.n_pages) {
+            raise_device_error(kErrKv8Page);
+            return -1;
+        }
+        return (int)((((uint32_t)pid * a.hkv + g) << a.lgp) | (uint32_t)(p & ((1 << a.lgp) - 1)));
+    }
 };
 
-__device__ __forceinline__ Kv8List kv8_list(const Kv8AttnArgs& a, int64_t q, int g) {
-    Kv8List r;
+__device__ __forceinline__ Kv8Keys<true> kv8_list(const Kv8AttnArgs& a, int64_t q, int g) {
+    Kv8Keys<true> r{};
     int64_t b = a.seq ? (int64_t)__ldg(a.seq + q) : q;
     const bool ok = b >= 0 && b < a.n_seq;
     if (!ok) {
@@ -290,322 +330,88 @@ __device__ __forceinline__ Kv8List kv8_list(const Kv8AttnArgs& a, int64_t q, int
     r.list = ok ? a.idx + (q * a.hkv + g) * (int64_t)a.n_idx : nullptr;
     r.table = a.table + b * a.max_pages;
     r.len = __ldg(a.lens + b);
-    r.n_idx = a.n_idx; r.max_pages = a.max_pages; r.hkv = a.hkv; r.g = g; r.lgp = a.lgp; r.n_pages = a.n_pages;
+    r.n_idx = a.n_idx;
+    r.g = g;
     return r;
 }
 
-__device__ __forceinline__ int kv8_entry(const Kv8List& r, int tile, int tend) {
-    const int e = tile * 16 + (threadIdx.x & 15);
-    return r.list != nullptr && tile < tend && e < r.n_idx ? __ldg(r.list + e) : -1;
-}
-
-__device__ __forceinline__ int kv8_row(const Kv8List& r, int p) {
-    if (p < 0) return -1;
-    const int pg = p >> r.lgp;
-    if (p >= r.len || pg >= r.max_pages) {
-        raise_device_error(kErrIndexRange);
-        return -1;
-    }
-    const int pid = __ldg(r.table + pg);
-    if (pid < 0 || pid >= r.n_pages) {
-        raise_device_error(kErrKv8Page);
-        return -1;
-    }
-    return (int)((((uint32_t)pid * r.hkv + r.g) << r.lgp) | (uint32_t)(p & ((1 << r.lgp) - 1)));
-}
-
+// The two scales of a row as bf16 halves (they are powers of two).
 __device__ __forceinline__ uint32_t kv8_scales(const Kv8AttnArgs& a, int row) {
-    if (row < 0) return 0u;
     const float2 s = __ldg(reinterpret_cast<const float2*>(a.scale) + (row >> a.lgp));
     return __byte_perm(__float_as_uint(s.x), __float_as_uint(s.y), 0x7632);  // K's upper half low, V's high
 }
 
-__device__ __forceinline__ void kv8_load_k_rows(const Kv8AttnArgs& a, int row, uint4 (&k)[4]) {
-    const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
-    const int r0 = __shfl_sync(0xffffffffu, row, gq), r1 = __shfl_sync(0xffffffffu, row, gq + 8);
-    const uint8_t* p0 = a.K + (int64_t)r0 * kD + 16 * tq;
-    const uint8_t* p1 = a.K + (int64_t)r1 * kD + 16 * tq;
-    k[0] = ldg_codes(p0, r0 >= 0);
-    k[1] = ldg_codes(p0 + 64, r0 >= 0);
-    k[2] = ldg_codes(p1, r1 >= 0);
-    k[3] = ldg_codes(p1 + 64, r1 >= 0);
+// Which of the 32 entries are keys, and a row for every lane.  A lane without
+// a key takes the row of a key of its 16-entry step (row 0 if the step has
+// none and is skipped), so that copies need no predicate and what they bring
+// is multiplied by a probability of 0 only where that row is attended anyway.
+__device__ __forceinline__ unsigned kv8_fill_rows(int& row) {
+    const unsigned valid = __ballot_sync(0xffffffffu, row >= 0);
+    if (valid != 0xffffffffu) {
+        const int step = threadIdx.x & 16;
+        const unsigned mine = (valid >> step) & 0xFFFFu;
+        const int other = __shfl_sync(0xffffffffu, row, step + (mine ? __ffs(mine) - 1 : 0));
+        if (row < 0) row = max(other, 0);
+    }
+    return valid;
 }
 
-__device__ __forceinline__ void kv8_load_v_rows(const Kv8AttnArgs& a, int row, uint4 (&v)[4]) {
-    const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = __shfl_sync(0xffffffffu, row, 2 * tq + (i & 1) + 8 * (i >> 1));
-        v[i] = ldg_codes(a.V + (int64_t)r * kD + 16 * gq, r >= 0);
-    }
-}
+// ------------------------------------------------- a warp's ring of steps
 
-// Tiles [t, tend) of one list into the warp's state.
-template <int FMT>
-__device__ __forceinline__ void kv8_list_tiles(const Kv8AttnArgs& a, const Kv8List& r, int t, int tend, Kv8State<1>& s) {
-    const int lane = threadIdx.x & 31, gq = lane >> 2;
-    if (t >= tend) return;
-    uint4 kc[4], vc[4];
-    int row = kv8_row(r, kv8_entry(r, t, tend));
-    int row1 = kv8_row(r, kv8_entry(r, t + 1, tend));
-    int e2 = kv8_entry(r, t + 2, tend);
-    uint32_t sc = kv8_scales(a, row);
-    kv8_load_k_rows(a, row, kc);
-    kv8_load_v_rows(a, row, vc);
-    for (; t < tend; ++t) {
-        uint4 kn[4], vn[4];
-        const int e3 = kv8_entry(r, t + 3, tend);
-        const int row2 = kv8_row(r, e2);
-        const uint32_t sc1 = kv8_scales(a, row1);
-        kv8_load_k_rows(a, row1, kn);
-        const unsigned valid = __ballot_sync(0xffffffffu, row >= 0);
-        float x[1][4];
-        uint32_t pb[1][2] = {{0u, 0u}};
-        if (valid) {
-            kv8_scores<FMT, 1>(s, kc, x);
-            const uint32_t c0 = __shfl_sync(0xffffffffu, sc, gq), c1 = __shfl_sync(0xffffffffu, sc, gq + 8);
-            const bool v0 = (valid >> gq) & 1u, v1 = (valid >> (gq + 8)) & 1u;
-            const float k0 = __uint_as_float(c0 << 16), k1 = __uint_as_float(c1 << 16);
-            x[0][0] = v0 ? x[0][0] * (k0 * s.cf[0][0]) : -CUDART_INF_F;
-            x[0][1] = v0 ? x[0][1] * (k0 * s.cf[0][1]) : -CUDART_INF_F;
-            x[0][2] = v1 ? x[0][2] * (k1 * s.cf[0][0]) : -CUDART_INF_F;
-            x[0][3] = v1 ? x[0][3] * (k1 * s.cf[0][1]) : -CUDART_INF_F;
-            // the step's largest V scale: positive floats order as integers
-            const float vmax = __uint_as_float(__reduce_max_sync(0xffffffffu, sc & 0xFFFF0000u));
-            kv8_softmax<1>(s, x, __uint_as_float(c0 & 0xFFFF0000u), __uint_as_float(c1 & 0xFFFF0000u), vmax, pb);
-        }
-        kv8_load_v_rows(a, row1, vn);
-        if (valid) kv8_pv<FMT, 1>(s, vc, pb);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) { kc[i] = kn[i]; vc[i] = vn[i]; }
-        row = row1; row1 = row2; e2 = e3; sc = sc1;
-    }
-}
+// Steps of 16 keys travel through a per-warp ring in shared memory: 16 rows of
+// K and 16 of V, 128 bytes each, the 16-byte chunk c of row r at c ^ (r & 7),
+// which makes both the copies and the operand reads free of bank conflicts.
+constexpr int kKv8Stages = 3;
+constexpr int kKv8Step = 16 * kD;                       // bytes of K (or V) in a step
+constexpr int kKv8Ring = kKv8Stages * 2 * kKv8Step;     // bytes of a warp's ring
 
-// Many rows: one warp per (query, kv-head), kv-head major so that the warps
-// resident at one time read one head's rows, which keeps them in L2.
-template <int FMT>
-__global__ void __launch_bounds__(32 * kKv8Warps, 2) kv8_list_kernel(Kv8AttnArgs a) {
-    const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
-    const int64_t wg = (int64_t)blockIdx.x * kKv8Warps + (threadIdx.x >> 5);
-    if (wg >= a.nq * a.hkv) return;
-    const int64_t q = wg % a.nq;
-    const int g = (int)(wg / a.nq);
-    const int hq = a.G * a.hkv;
-    Kv8State<1> s;
-    const uint16_t* const row[1] = {gq < a.G ? a.Q + q * a.q_stride + (int64_t)(g * a.G + gq) * kD : nullptr};
-    kv8_load_q<1>(s, row, a.scale_log2);
-    const Kv8List r = kv8_list(a, q, g);
-    kv8_list_tiles<FMT>(a, r, 0, (a.n_idx + 15) / 16, s);
-    kv8_reduce_l<1>(s);
+// Copies of step `st` (0, 1) of the 32 rows into ring slot `slot`.
+__device__ __forceinline__ void kv8_issue(const Kv8AttnArgs& a, uint32_t ring, int slot, int row, int st, unsigned valid) {
+    const int lane = threadIdx.x & 31, r0 = lane >> 3, c = lane & 7;
+    if (valid) {
+        const uint32_t dst = ring + slot * 2 * kKv8Step;
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        if (2 * tq + c >= a.G) continue;
-        const float l = s.l[0][c], f = l > 0.f || l != l ? s.vref / l : 0.f;
-        const int64_t orow = q * hq + g * a.G + 2 * tq + c;
-        uint32_t w[8];
-#pragma unroll
-        for (int mt = 0; mt < 8; ++mt) w[mt] = pack_bf16x2(s.o[0][mt][c] * f, s.o[0][mt][2 + c] * f);
-        uint4* op = reinterpret_cast<uint4*>(a.O + orow * kD + 16 * gq);
-        op[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        op[1] = make_uint4(w[4], w[5], w[6], w[7]);
-        if (a.lse && gq == 0) a.lse[orow] = l > 0.f || l != l ? s.m[0][c] - kKv8Head + log2f(l) : -CUDART_INF_F;
-    }
-}
-
-// ------------------------------------------------ rows split over the GPU
-
-// The work is one stream of 16-key tiles: rows in the order (sequence,
-// kv-head, column group), each with the tiles its mask leaves (at least one).
-// CTA c takes tiles [c per, (c + 1) per): the same work for every CTA however
-// ragged the lengths.  A row inside one CTA's range is finished there; a row
-// that crosses CTAs leaves a partial state in every CTA it touches (slot 0 if
-// it began before the CTA, slot 1 if it began inside), and kv8_join_kernel
-// joins them.  Everyone derives the stream from lens and cu by the same scan.
-struct Kv8Seq {
-    int64_t base;     // first tile of the sequence in the stream
-    int32_t tiles;    // tiles of each of its rows
-    int32_t rows;     // hkv * column groups
-    int32_t groups;
-    int32_t n, len;   // new tokens, tokens in all
-    int64_t q0;
-    int32_t n_sink, t_lo;  // tiles [0, n_sink) and from t_lo on
-};
-
-template <int NT, bool LIST>
-__device__ __forceinline__ void kv8_seq(const Kv8AttnArgs& a, int64_t b, Kv8Seq& q) {
-    if constexpr (LIST) {  // "sequence" b is query b
-        q.n = 1; q.q0 = b; q.len = 0; q.groups = 1; q.rows = a.hkv; q.n_sink = 0; q.t_lo = 0;
-        q.tiles = max(1, (a.n_idx + 15) / 16);
-    } else {
-        q.q0 = a.cu ? (int64_t)__ldg(a.cu + b) : b;
-        int64_t n = a.cu ? (int64_t)__ldg(a.cu + b + 1) - q.q0 : 1;
-        int64_t len = __ldg(a.lens + b);
-        if (n < 0 || (n > 0 && (q.q0 < 0 || q.q0 + n > a.nq))) {
-            raise_device_error(kErrKv8Range);
-            n = 0;
-        }
-        if (len < 0 || len > ((int64_t)a.max_pages << a.lgp)) {
-            raise_device_error(kErrKv8Range);
-            len = len < 0 ? 0 : (int64_t)a.max_pages << a.lgp;
-        }
-        q.n = (int)n;
-        q.len = (int)len;
-        q.groups = (int)((n * a.G + 8 * NT - 1) / (8 * NT));
-        q.rows = a.hkv * q.groups;
-        const int hi = (int)((len + 15) / 16);
-        const int64_t lo = a.W > 0 ? len - n - a.W + 1 : 0;  // the first query's window begins there
-        q.t_lo = lo > 0 ? (int)(lo / 16) : 0;
-        q.n_sink = min((min(a.S, (int)len) + 15) / 16, q.t_lo);
-        q.tiles = max(1, q.n_sink + hi - q.t_lo);
-    }
-}
-
-template <int NT, bool LIST>
-struct Kv8Scan {
-    int64_t total, per;
-    // Tiles of all sequences, and each CTA's share of them.  `least`: tiles a
-    // CTA takes at least.
-    __device__ __forceinline__ void init(const Kv8AttnArgs& a, int n_cta, int least) {
-        if constexpr (LIST) {
-            Kv8Seq q;
-            kv8_seq<NT, true>(a, 0, q);
-            total = a.nq * a.hkv * (int64_t)q.tiles;
-        } else {
-            __shared__ long long sum[kKv8Warps];
-            long long mine = 0;
-            for (int64_t b = threadIdx.x; b < a.n_seq; b += 32 * kKv8Warps) {
-                Kv8Seq q;
-                kv8_seq<NT, false>(a, b, q);
-                mine += (int64_t)q.tiles * q.rows;
-            }
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, off);
-            if ((threadIdx.x & 31) == 0) sum[threadIdx.x >> 5] = mine;
-            __syncthreads();
-            total = 0;
-#pragma unroll
-            for (int i = 0; i < kKv8Warps; ++i) total += sum[i];
-            __syncthreads();
-        }
-        per = max((int64_t)least, (total + n_cta - 1) / n_cta);
-    }
-    // The sequence whose tiles hold position w of the stream (0 <= w < total).
-    __device__ __forceinline__ int64_t find(const Kv8AttnArgs& a, int64_t w, Kv8Seq& out) {
-        if constexpr (LIST) {
-            kv8_seq<NT, true>(a, 0, out);
-            const int64_t b = w / ((int64_t)out.tiles * out.rows);
-            kv8_seq<NT, true>(a, b, out);
-            out.base = b * out.tiles * out.rows;
-            return b;
-        } else {
-            __shared__ long long wsum[kKv8Warps];
-            __shared__ long long fb, fbase;
-            const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-            long long base = 0;
-            for (int64_t b0 = 0; b0 < a.n_seq; b0 += 32 * kKv8Warps) {
-                const int64_t b = b0 + threadIdx.x;
-                long long m = 0;
-                if (b < a.n_seq) {
-                    Kv8Seq q;
-                    kv8_seq<NT, false>(a, b, q);
-                    m = (int64_t)q.tiles * q.rows;
-                }
-                long long inc = m;
-#pragma unroll
-                for (int off = 1; off < 32; off <<= 1) {
-                    const long long up = __shfl_up_sync(0xffffffffu, inc, off);
-                    if (lane >= off) inc += up;
-                }
-                if (lane == 31) wsum[wid] = inc;
-                __syncthreads();
-                long long before = base, all = base;
-#pragma unroll
-                for (int i = 0; i < kKv8Warps; ++i) {
-                    if (i < wid) before += wsum[i];
-                    all += wsum[i];
-                }
-                const long long first = before + inc - m;
-                if (w >= first && w < first + m) { fb = b; fbase = first; }
-                __syncthreads();
-                base = all;
-                if (w < base) break;  // uniform: every thread holds the same sums
-            }
-            const int64_t b = fb;
-            kv8_seq<NT, false>(a, b, out);
-            out.base = fbase;
-            __syncthreads();
-            return b;
+        for (int i = 0; i < 4; ++i) {
+            const int r = 4 * i + r0;
+            const int64_t off = (int64_t)__shfl_sync(0xffffffffu, row, 16 * st + r) * kD + 16 * c;
+            const uint32_t at = dst + r * kD + ((c ^ (r & 7)) << 4);
+            cp_async_16(at, a.K + off, 16);
+            cp_async_16(at + kKv8Step, a.V + off, 16);
         }
     }
-};
-
-// Keys of one dense tile: page row of the first (-1: none), its scales.
-struct Kv8Dense {
-    const int32_t* table;
-    int32_t len, n_sink, t_lo, g;
-};
-
-__device__ __forceinline__ int kv8_tile_key(const Kv8Dense& d, int t) {
-    return 16 * (t < d.n_sink ? t : t - d.n_sink + d.t_lo);
+    cp_async_commit();
 }
 
-__device__ __forceinline__ int kv8_tile_page(const Kv8AttnArgs& a, const Kv8Dense& d, int t, int tend) {
-    const int key = kv8_tile_key(d, t);
-    return t < tend && key < d.len ? __ldg(d.table + (key >> a.lgp)) : -2;
+__device__ __forceinline__ uint4 lds_16(uint32_t p) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p));
+    return v;
 }
 
-__device__ __forceinline__ int kv8_tile_row(const Kv8AttnArgs& a, const Kv8Dense& d, int t, int pid) {
-    if (pid == -2) return -1;
-    if (pid < 0 || pid >= a.n_pages) {
-        raise_device_error(kErrKv8Page);
-        return -1;
-    }
-    return (int)((((uint32_t)pid * a.hkv + d.g) << a.lgp) | (uint32_t)(kv8_tile_key(d, t) & ((1 << a.lgp) - 1)));
-}
-
-// Keys of a tile that some column of the row attends: bit i = key i.
-struct Kv8Mask {
-    int tmin, tmax, lo, S;  // positions of the row's first and last query; first key of the first one's window
-};
-
-__device__ __forceinline__ unsigned kv8_tile_mask(const Kv8Mask& k, int key, int row) {
-    if (row < 0 || key > k.tmax) return 0u;
-    unsigned m = k.tmax - key >= 15 ? 0xFFFFu : (2u << (k.tmax - key)) - 1u;
-    if (key < k.lo) {  // below the window only the sinks
-        const unsigned below = k.lo - key >= 16 ? 0xFFFFu : (1u << (k.lo - key)) - 1u;
-        const unsigned sink = k.S - key >= 16 ? 0xFFFFu : k.S > key ? (1u << (k.S - key)) - 1u : 0u;
-        m &= ~below | sink;
-    }
-    return m;
-}
-
-__device__ __forceinline__ void kv8_load_k_tile(const Kv8AttnArgs& a, int row, unsigned m, uint4 (&k)[4]) {
+__device__ __forceinline__ void kv8_read_k(uint32_t slot, Kv8K& k) {
     const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
-    const uint8_t* p = a.K + ((int64_t)row + gq) * kD + 16 * tq;
-    const bool v0 = (m >> gq) & 1u, v1 = (m >> (gq + 8)) & 1u;
-    k[0] = ldg_codes(p, v0);
-    k[1] = ldg_codes(p + 64, v0);
-    k[2] = ldg_codes(p + 8 * kD, v1);
-    k[3] = ldg_codes(p + 8 * kD + 64, v1);
+    const uint32_t p = slot + gq * kD + (((2 * tq) ^ gq) << 4);
+    k.a[0] = lds_16(p);
+    k.a[1] = lds_16(p ^ 16u);
+    k.b[0] = lds_16(p + 8 * kD);
+    k.b[1] = lds_16((p ^ 16u) + 8 * kD);
 }
 
-__device__ __forceinline__ void kv8_load_v_tile(const Kv8AttnArgs& a, int row, unsigned m, uint4 (&v)[4]) {
+__device__ __forceinline__ void kv8_read_v(uint32_t slot, uint4 (&v)[4]) {
     const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
-    const uint8_t* p = a.V + ((int64_t)row + 2 * tq) * kD + 16 * gq;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int off = (i & 1) + 8 * (i >> 1);
-        v[i] = ldg_codes(p + off * kD, (m >> (2 * tq + off)) & 1u);
-    }
+    const uint32_t p = slot + kKv8Step + 2 * tq * kD + ((gq ^ (2 * tq)) << 4);
+    v[0] = lds_16(p);
+    v[1] = lds_16((p ^ 16u) + kD);
+    v[2] = lds_16(p + 8 * kD);
+    v[3] = lds_16((p ^ 16u) + 9 * kD);
 }
 
-// O^T += V^T P^T for a tile whose mask differs between columns and which holds
+// O^T += V^T P^T for a step whose mask differs between columns and which holds
 // a NaN value: column by column, so that a NaN under one column's mask does
 // not reach it through 0 * NaN.
 template <int FMT, int NT>
 __device__ __forceinline__ void kv8_pv_columns(Kv8State<NT>& s, const uint4 (&v)[4], const uint32_t (&pb)[NT][2],
-                                            const int (&tc)[NT][2], int key, int W, int S) {
+                                               const int (&tc)[NT][2], int key, int W, int S) {
     const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -638,70 +444,260 @@ __device__ __forceinline__ void kv8_pv_columns(Kv8State<NT>& s, const uint4 (&v)
         }
 }
 
-// Tiles [t, tend) of one dense row into the warp's state; tc: the positions
-// of the lane's columns (-1: no such column).
-template <int FMT, int NT>
-__device__ __forceinline__ void kv8_dense_tiles(const Kv8AttnArgs& a, const Kv8Dense& d, const Kv8Mask& mk,
-                                                const int (&tc)[NT][2], int t, int tend, Kv8State<NT>& s) {
-    const int lane = threadIdx.x & 31, gq = lane >> 2;
-    if (t >= tend) return;
-    uint4 kc[4], vc[4];
-    int row = kv8_tile_row(a, d, t, kv8_tile_page(a, d, t, tend));
-    int pid1 = kv8_tile_page(a, d, t + 1, tend);
-    unsigned m = kv8_tile_mask(mk, kv8_tile_key(d, t), row);
-    float2 sc = row >= 0 ? __ldg(reinterpret_cast<const float2*>(a.scale) + (row >> a.lgp)) : make_float2(0.f, 0.f);
-    kv8_load_k_tile(a, row, m, kc);
-    kv8_load_v_tile(a, row, m, vc);
-    for (; t < tend; ++t) {
-        uint4 kn[4], vn[4];
-        const int pid2 = kv8_tile_page(a, d, t + 2, tend);
-        const int row1 = kv8_tile_row(a, d, t + 1, pid1);
-        const unsigned m1 = kv8_tile_mask(mk, kv8_tile_key(d, t + 1), row1);
-        const float2 sc1 = row1 >= 0 ? __ldg(reinterpret_cast<const float2*>(a.scale) + (row1 >> a.lgp)) : make_float2(0.f, 0.f);
-        kv8_load_k_tile(a, row1, m1, kn);
-        float x[NT][4];
-        uint32_t pb[NT][2];
-        const int key = kv8_tile_key(d, t);
-        // every column attends all 16 keys
-        const bool whole = m == 0xFFFFu && key + 15 <= mk.tmin && (a.W == 0 || key >= mk.lo + (mk.tmax - mk.tmin) || key + 16 <= mk.S);
-        if (m) {
-            kv8_scores<FMT, NT>(s, kc, x);
+// One step.  sc: the 32 rows' scales; valid: the step's 16 keys; tc (dense):
+// positions of the lane's columns, -1 for no column; key: the step's first.
+template <int FMT, int NT, bool LIST>
+__device__ __forceinline__ void kv8_step(const Kv8AttnArgs& a, const Kv8Keys<LIST>& r, Kv8State<NT>& s, uint32_t slot,
+                                         uint32_t sc, int st, unsigned valid, const int (&tc)[NT][2], int key) {
+    const int gq = (threadIdx.x & 31) >> 2;
+    Kv8K k;
+    kv8_read_k(slot, k);
+    float x[NT][4];
+    kv8_scores<FMT, NT>(s, k, x);
+    const uint32_t c0 = __shfl_sync(0xffffffffu, sc, 16 * st + gq), c1 = __shfl_sync(0xffffffffu, sc, 16 * st + gq + 8);
+    const float k0 = __uint_as_float(c0 << 16), k1 = __uint_as_float(c1 << 16);
+    // dense: every column attends all 16 keys
+    const bool whole = valid == 0xFFFFu &&
+                       (LIST || (key + 15 <= r.tmin && (a.W == 0 || key >= r.lo + (r.tmax - r.tmin) || key + 16 <= a.S)));
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const float f0 = sc.x * s.cf[nt][0], f1 = sc.x * s.cf[nt][1];
+    for (int nt = 0; nt < NT; ++nt) {
+        x[nt][0] *= k0 * s.cf[nt][0];
+        x[nt][1] *= k0 * s.cf[nt][1];
+        x[nt][2] *= k1 * s.cf[nt][0];
+        x[nt][3] *= k1 * s.cf[nt][1];
+        if (!whole) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x[nt][i] *= (i & 1) ? f1 : f0;
-                if (!whole) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int j = key + gq + 8 * (i >> 1), tt = tc[nt][i & 1];
-                        const bool ok = ((m >> (j - key)) & 1u) && j <= tt && (a.W == 0 || j > tt - a.W || j < a.S);
-                        if (!ok) x[nt][i] = -CUDART_INF_F;
-                    }
+            for (int i = 0; i < 4; ++i) {
+                const int j = gq + 8 * (i >> 1);
+                bool ok = (valid >> j) & 1u;
+                if constexpr (!LIST) {
+                    const int t = tc[nt][i & 1];
+                    ok = ok && key + j <= t && (a.W == 0 || key + j > t - a.W || key + j < a.S);
                 }
+                if (!ok) x[nt][i] = -CUDART_INF_F;
             }
-            kv8_softmax<NT>(s, x, sc.y, sc.y, sc.y, pb);
         }
-        kv8_load_v_tile(a, row1, m1, vn);
-        if (m) {
-            bool slow = false;
-            if constexpr (FMT == 0) {
-                if (!whole && mk.tmin != mk.tmax) {
+    }
+    const float v0 = __uint_as_float(c0 & 0xFFFF0000u), v1 = __uint_as_float(c1 & 0xFFFF0000u);
+    // the step's largest V scale: positive floats order as integers
+    float vmax = s.vref;
+    if (__any_sync(0xffffffffu, fmaxf(v0, v1) > s.vref))
+        vmax = __uint_as_float(__reduce_max_sync(0xffffffffu, max(c0, c1) & 0xFFFF0000u));
+    uint32_t pb[NT][2];
+    kv8_softmax<NT>(s, x, v0, v1, vmax, pb);
+    uint4 v[4];
+    kv8_read_v(slot, v);
+    if constexpr (FMT == 0 && !LIST) {
+        if (!whole && r.tmin != r.tmax) {
+            bool nan = false;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) slow = slow || __vcmpeq4(word_of(vc[i], j) & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0u;
-                    slow = __any_sync(0xffffffffu, slow);
-                }
+                for (int j = 0; j < 4; ++j) nan = nan || __vcmpeq4(word_of(v[i], j) & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0u;
+            if (__any_sync(0xffffffffu, nan)) {
+                kv8_pv_columns<FMT, NT>(s, v, pb, tc, key, a.W, a.S);
+                return;
             }
-            if (slow) kv8_pv_columns<FMT, NT>(s, vc, pb, tc, key, a.W, a.S);
-            else kv8_pv<FMT, NT>(s, vc, pb);
         }
+    }
+    kv8_pv<FMT, NT>(s, v, pb);
+}
+
+// Chunks [c, cend) of a row into the warp's state.  Copies run two steps ahead
+// of their use, the rows' table entries and scales a chunk further.
+template <int FMT, int NT, bool LIST>
+__device__ __forceinline__ void kv8_chunks(const Kv8AttnArgs& a, const Kv8Keys<LIST>& r, int c, int cend,
+                                           const int (&tc)[NT][2], Kv8State<NT>& s, uint32_t ring) {
+    if (c >= cend) return;
+    int row0 = r.row(a, r.entry(a, c, cend));
+    int row1 = r.row(a, r.entry(a, c + 1, cend));
+    int e2 = r.entry(a, c + 2, cend);
+    unsigned valid = kv8_fill_rows(row0);
+    kv8_issue(a, ring, 0, row0, 0, valid & 0xFFFFu);
+    kv8_issue(a, ring, 1, row0, 1, valid >> 16);
+    uint32_t sc = kv8_scales(a, row0);
+    int slot = 0;
+    for (; c < cend; ++c) {
+        const unsigned valid1 = kv8_fill_rows(row1);
+        const int key = LIST ? 0 : r.key0(c);
+        cp_async_wait<1>();
+        __syncwarp();
+        kv8_issue(a, ring, slot == 0 ? 2 : slot - 1, row1, 0, valid1 & 0xFFFFu);
+        const int e3 = r.entry(a, c + 3, cend);
+        if (valid & 0xFFFFu) kv8_step<FMT, NT, LIST>(a, r, s, ring + slot * 2 * kKv8Step, sc, 0, valid & 0xFFFFu, tc, key);
+        cp_async_wait<1>();
+        __syncwarp();
+        kv8_issue(a, ring, slot, row1, 1, valid1 >> 16);
+        const uint32_t sc1 = kv8_scales(a, row1);
+        const int row2 = r.row(a, e2);
+        slot = slot == 2 ? 0 : slot + 1;
+        if (valid >> 16) kv8_step<FMT, NT, LIST>(a, r, s, ring + slot * 2 * kKv8Step, sc, 1, valid >> 16, tc, key + 16);
+        slot = slot == 2 ? 0 : slot + 1;
+        row1 = row2; e2 = e3; sc = sc1; valid = valid1;
+    }
+    cp_async_wait<0>();
+    __syncwarp();
+}
+
+// Many rows: one warp per (query, kv-head), kv-head major so that the warps
+// resident at one time read one head's rows, which keeps them in L2.
+template <int FMT>
+__global__ void __launch_bounds__(32 * kKv8ListWarps, 2) kv8_list_kernel(Kv8AttnArgs a) {
+    const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
+    const int64_t wg = (int64_t)blockIdx.x * kKv8ListWarps + (threadIdx.x >> 5);
+    if (wg >= a.nq * a.hkv) return;
+    const int64_t q = wg % a.nq;
+    const int g = (int)(wg / a.nq);
+    const int hq = a.G * a.hkv;
+    Kv8State<1> s;
+    const uint16_t* const row[1] = {gq < a.G ? a.Q + q * a.q_stride + (int64_t)(g * a.G + gq) * kD : nullptr};
+    kv8_load_q<1>(s, row, a.scale_log2);
+    const Kv8Keys<true> r = kv8_list(a, q, g);
+    extern __shared__ __align__(1024) uint8_t lsm[];
+    const int tc[1][2] = {{0, 0}};
+    kv8_chunks<FMT, 1, true>(a, r, 0, (a.n_idx + 31) / 32, tc, s, smem_u32(lsm) + (threadIdx.x >> 5) * kKv8Ring);
+    kv8_reduce_l<1>(s);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) { kc[i] = kn[i]; vc[i] = vn[i]; }
-        row = row1; pid1 = pid2; m = m1; sc = sc1;
+    for (int c = 0; c < 2; ++c) {
+        if (2 * tq + c >= a.G) continue;
+        const float l = s.l[0][c], f = l > 0.f || l != l ? s.vref / l : 0.f;
+        const int64_t orow = q * hq + g * a.G + 2 * tq + c;
+        uint32_t w[8];
+#pragma unroll
+        for (int mt = 0; mt < 8; ++mt) w[mt] = pack_bf16x2(s.o[0][mt][c] * f, s.o[0][mt][2 + c] * f);
+        uint4* op = reinterpret_cast<uint4*>(a.O + orow * kD + 16 * gq);
+        op[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        op[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        if (a.lse && gq == 0) a.lse[orow] = l > 0.f || l != l ? s.m[0][c] - kKv8Head + log2f(l) : -CUDART_INF_F;
     }
 }
+
+// ------------------------------------------------ rows split over the GPU
+
+// The work is one stream of 32-key chunks: rows in the order (sequence,
+// kv-head, column group), each with the chunks its mask leaves (at least one).
+// CTA c takes chunks [c per, (c + 1) per): the same work for every CTA however
+// ragged the lengths.  A row inside one CTA's range is finished there; a row
+// that crosses CTAs leaves a partial state in every CTA it touches (slot 0 if
+// it began before the CTA, slot 1 if it began inside), and kv8_join_kernel
+// joins them.  Everyone derives the stream from lens and cu by the same scan.
+struct Kv8Seq {
+    int64_t base;     // first chunk of the sequence in the stream
+    int32_t chunks;   // chunks of each of its rows
+    int32_t rows;     // hkv * column groups
+    int32_t groups;
+    int32_t n, len;   // new tokens, tokens in all
+    int64_t q0;
+    int32_t n_sink, c_lo;  // chunks [0, n_sink) and from c_lo on
+};
+
+template <int NT, bool LIST>
+__device__ __forceinline__ void kv8_seq(const Kv8AttnArgs& a, int64_t b, Kv8Seq& q) {
+    if constexpr (LIST) {  // "sequence" b is query b
+        q.n = 1; q.q0 = b; q.len = 0; q.groups = 1; q.rows = a.hkv; q.n_sink = 0; q.c_lo = 0;
+        q.chunks = max(1, (a.n_idx + 31) / 32);
+    } else {
+        q.q0 = a.cu ? (int64_t)__ldg(a.cu + b) : b;
+        int64_t n = a.cu ? (int64_t)__ldg(a.cu + b + 1) - q.q0 : 1;
+        int64_t len = __ldg(a.lens + b);
+        if (n < 0 || (n > 0 && (q.q0 < 0 || q.q0 + n > a.nq))) {
+            raise_device_error(kErrKv8Range);
+            n = 0;
+        }
+        if (len < 0 || len > ((int64_t)a.max_pages << a.lgp)) {
+            raise_device_error(kErrKv8Range);
+            len = len < 0 ? 0 : (int64_t)a.max_pages << a.lgp;
+        }
+        q.n = (int)n;
+        q.len = (int)len;
+        q.groups = (int)((n * a.G + 8 * NT - 1) / (8 * NT));
+        q.rows = a.hkv * q.groups;
+        const int hi = (int)((len + 31) / 32);
+        const int64_t lo = a.W > 0 ? len - n - a.W + 1 : 0;  // the first query's window begins there
+        q.c_lo = lo > 0 ? (int)(lo / 32) : 0;
+        q.n_sink = min((min(a.S, (int)len) + 31) / 32, q.c_lo);
+        q.chunks = max(1, q.n_sink + hi - q.c_lo);
+    }
+}
+
+template <int NT, bool LIST>
+struct Kv8Scan {
+    int64_t total, per;
+    // Chunks of all sequences, and each CTA's share of them.  `least`: chunks a
+    // CTA takes at least.
+    __device__ __forceinline__ void init(const Kv8AttnArgs& a, int n_cta, int least) {
+        if constexpr (LIST) {
+            Kv8Seq q;
+            kv8_seq<NT, true>(a, 0, q);
+            total = a.nq * a.hkv * (int64_t)q.chunks;
+        } else {
+            __shared__ long long sum[kKv8Warps];
+            long long mine = 0;
+            for (int64_t b = threadIdx.x; b < a.n_seq; b += 32 * kKv8Warps) {
+                Kv8Seq q;
+                kv8_seq<NT, false>(a, b, q);
+                mine += (int64_t)q.chunks * q.rows;
+            }
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, off);
+            if ((threadIdx.x & 31) == 0) sum[threadIdx.x >> 5] = mine;
+            __syncthreads();
+            total = 0;
+#pragma unroll
+            for (int i = 0; i < kKv8Warps; ++i) total += sum[i];
+            __syncthreads();
+        }
+        per = max((int64_t)least, (total + n_cta - 1) / n_cta);
+    }
+    // The sequence whose chunks hold position w of the stream (0 <= w < total).
+    __device__ __forceinline__ int64_t find(const Kv8AttnArgs& a, int64_t w, Kv8Seq& out) {
+        if constexpr (LIST) {
+            kv8_seq<NT, true>(a, 0, out);
+            const int64_t b = w / ((int64_t)out.chunks * out.rows);
+            kv8_seq<NT, true>(a, b, out);
+            out.base = b * out.chunks * out.rows;
+            return b;
+        } else {
+            __shared__ long long wsum[kKv8Warps];
+            __shared__ long long fb, fbase;
+            const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+            long long base = 0;
+            for (int64_t b0 = 0; b0 < a.n_seq; b0 += 32 * kKv8Warps) {
+                const int64_t b = b0 + threadIdx.x;
+                long long m = 0;
+                if (b < a.n_seq) {
+                    Kv8Seq q;
+                    kv8_seq<NT, false>(a, b, q);
+                    m = (int64_t)q.chunks * q.rows;
+                }
+                long long inc = m;
+#pragma unroll
+                for (int off = 1; off < 32; off <<= 1) {
+                    const long long up = __shfl_up_sync(0xffffffffu, inc, off);
+                    if (lane >= off) inc += up;
+                }
+                if (lane == 31) wsum[wid] = inc;
+                __syncthreads();
+                long long before = base, all = base;
+#pragma unroll
+                for (int i = 0; i < kKv8Warps; ++i) {
+                    if (i < wid) before += wsum[i];
+                    all += wsum[i];
+                }
+                const long long first = before + inc - m;
+                if (w >= first && w < first + m) { fb = b; fbase = first; }
+                __syncthreads();
+                base = all;
+                if (w < base) break;  // uniform: every thread holds the same sums
+            }
+            const int64_t b = fb;
+            kv8_seq<NT, false>(a, b, out);
+            out.base = fbase;
+            __syncthreads();
+            return b;
+        }
+    }
+};
 
 constexpr int kKv8Pad = kD + 4;  // floats per column in shared memory: consecutive columns start 4 banks apart
 
@@ -725,9 +721,11 @@ __device__ __forceinline__ void kv8_store(const Kv8AttnArgs& a, int64_t orow, in
 
 template <int FMT, int NT, bool LIST>
 __global__ void __launch_bounds__(32 * kKv8Warps, NT == 1 ? 2 : 1) kv8_split_kernel(Kv8AttnArgs a, int least) {
-    extern __shared__ __align__(16) float ksm[];
-    float* so = ksm;                                              // [warps][8 NT][kKv8Pad]
-    float* sml = ksm + kKv8Warps * 8 * NT * kKv8Pad;              // [warps][8 NT][2]
+    extern __shared__ __align__(1024) uint8_t ksm[];
+    __shared__ float sml[kKv8Warps * 8 * NT * 2];                 // (m, l) of every warp's columns
+    const uint32_t ring = smem_u32(ksm) + (threadIdx.x >> 5) * kKv8Ring;
+    // a warp's sums go where its ring was: [8 NT][kKv8Pad] floats
+    auto so = [&](int w) { return reinterpret_cast<float*>(ksm + w * kKv8Ring); };
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, gq = lane >> 2, tq = lane & 3;
     Kv8Scan<NT, LIST> scan;
     scan.init(a, (int)gridDim.x, least);
@@ -736,15 +734,15 @@ __global__ void __launch_bounds__(32 * kKv8Warps, NT == 1 ? 2 : 1) kv8_split_ker
     Kv8Seq q;
     int64_t b = scan.find(a, w0, q);
     for (int64_t w = w0; w < w1;) {
-        while (w >= q.base + (int64_t)q.tiles * q.rows) {  // the next sequence that has rows
-            const int64_t next = q.base + (int64_t)q.tiles * q.rows;
+        while (w >= q.base + (int64_t)q.chunks * q.rows) {  // the next sequence that has rows
+            const int64_t next = q.base + (int64_t)q.chunks * q.rows;
             kv8_seq<NT, LIST>(a, ++b, q);
             q.base = next;
         }
         const int64_t rel = w - q.base;
-        const int r = (int)(rel / q.tiles), t0 = (int)(rel % q.tiles);
+        const int r = (int)(rel / q.chunks), t0 = (int)(rel % q.chunks);
         const int g = r / q.groups, cg = r % q.groups;
-        const int n = (int)min((int64_t)(q.tiles - t0), w1 - w);
+        const int n = (int)min((int64_t)(q.chunks - t0), w1 - w);
         const int ta = t0 + (int)((int64_t)n * wid / kKv8Warps), tb = t0 + (int)((int64_t)n * (wid + 1) / kKv8Warps);
 
         if (ta < tb) {
@@ -758,18 +756,21 @@ __global__ void __launch_bounds__(32 * kKv8Warps, NT == 1 ? 2 : 1) kv8_split_ker
             }
             const uint16_t* const (&crow)[NT] = row;
             kv8_load_q<NT>(s, crow, a.scale_log2);
+            Kv8Keys<LIST> keys{};
+            int tc[NT][2] = {};
             if constexpr (LIST) {
-                const Kv8List lr = kv8_list(a, q.q0, g);
-                kv8_list_tiles<FMT>(a, lr, ta, tb, s);
+                keys = kv8_list(a, q.q0, g);
             } else {
                 const int first = q.len - q.n;  // position of the sequence's first query
                 const int c0 = cg * 8 * NT, c1 = min((int)(q.n * a.G), c0 + 8 * NT) - 1;
-                Kv8Mask mk;
-                mk.tmin = first + c0 / a.G;
-                mk.tmax = first + c1 / a.G;
-                mk.lo = a.W > 0 ? mk.tmin - a.W + 1 : 0;
-                mk.S = a.S;
-                int tc[NT][2];
+                keys.table = a.table + b * a.max_pages;
+                keys.len = q.len;
+                keys.g = g;
+                keys.n_sink = q.n_sink;
+                keys.c_lo = q.c_lo;
+                keys.tmin = first + c0 / a.G;
+                keys.tmax = first + c1 / a.G;
+                keys.lo = a.W > 0 ? keys.tmin - a.W + 1 : 0;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -777,16 +778,15 @@ __global__ void __launch_bounds__(32 * kKv8Warps, NT == 1 ? 2 : 1) kv8_split_ker
                         const int cc = c0 + 8 * nt + 2 * tq + c;
                         tc[nt][c] = cc <= c1 ? first + cc / a.G : -1;
                     }
-                const Kv8Dense d{a.table + b * a.max_pages, q.len, q.n_sink, q.t_lo, g};
-                kv8_dense_tiles<FMT, NT>(a, d, mk, tc, ta, tb, s);
             }
+            kv8_chunks<FMT, NT, LIST>(a, keys, ta, tb, tc, s, ring);
             kv8_reduce_l<NT>(s);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     const int col = wid * 8 * NT + 8 * nt + 2 * tq + c;
-                    float4* p = reinterpret_cast<float4*>(so + col * kKv8Pad + 16 * gq);
+                    float4* p = reinterpret_cast<float4*>(so(wid) + (8 * nt + 2 * tq + c) * kKv8Pad + 16 * gq);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         p[j] = make_float4(s.o[nt][2 * j][c] * s.vref, s.o[nt][2 * j][2 + c] * s.vref,
@@ -796,11 +796,11 @@ __global__ void __launch_bounds__(32 * kKv8Warps, NT == 1 ? 2 : 1) kv8_split_ker
         } else {
             for (int col = lane; col < 8 * NT; col += 32) {
                 sml[2 * (wid * 8 * NT + col)] = -FLT_MAX;
-                sml[2 * (wid * 8 * NT + col) + 1] = -1.f;  // took no tile
+                sml[2 * (wid * 8 * NT + col) + 1] = -1.f;  // took no chunk
             }
         }
         __syncthreads();
-        const bool final_ = n == q.tiles;
+        const bool final_ = n == q.chunks;
         float* part = a.part + ((int64_t)blockIdx.x * 2 + (t0 == 0 ? 1 : 0)) * kv8_part_floats<NT>();
         for (int e = tid; e < 8 * NT * kD; e += 32 * kKv8Warps) {
             const int c = e / kD, dim = e % kD;
@@ -814,9 +814,9 @@ __global__ void __launch_bounds__(32 * kKv8Warps, NT == 1 ? 2 : 1) kv8_split_ker
                 const int col = i * 8 * NT + c;
                 const float li = sml[2 * col + 1];
                 if (li == -1.f) continue;
-                const float f = exp2f(sml[2 * col] - M);
+                const float f = ex2(sml[2 * col] - M);
                 l += li * f;
-                acc += so[col * kKv8Pad + dim] * f;
+                acc += so(i)[c * kKv8Pad + dim] * f;
             }
             if (final_) {
                 kv8_store(a, orow, dim, acc, M, l);
@@ -840,11 +840,11 @@ __global__ void __launch_bounds__(32 * kKv8Warps) kv8_join_kernel(Kv8AttnArgs a,
     if (w1 >= scan.total) return;
     Kv8Seq q;
     scan.find(a, w1, q);
-    const int64_t r = (w1 - q.base) / q.tiles;
-    const int64_t begin = q.base + r * q.tiles, end = begin + q.tiles;
+    const int64_t r = (w1 - q.base) / q.chunks;
+    const int64_t begin = q.base + r * q.chunks, end = begin + q.chunks;
     if (begin == w1 || begin < w0) return;
     const int g = (int)(r / q.groups), cg = (int)(r % q.groups);
-    const int more = (int)((end - 1) / scan.per - c);  // CTAs after c that hold tiles of the row
+    const int more = (int)((end - 1) / scan.per - c);  // CTAs after c that hold chunks of the row
     const int e = blockIdx.y * 128 + (threadIdx.x & 127), half = threadIdx.x >> 7;
     const int col = e / kD, dim = e % kD;
     const int64_t orow = kv8_out_row<NT>(a, q, cg, g, col);
@@ -858,7 +858,7 @@ __global__ void __launch_bounds__(32 * kKv8Warps) kv8_join_kernel(Kv8AttnArgs a,
     for (int i = half; i <= more; i += 2) {
         const float* p = at(i);
         const float mi = p[8 * NT * kD + 2 * col], li = p[8 * NT * kD + 2 * col + 1], x = p[col * kD + dim];
-        const float n = fmaxf(M, mi), fa = exp2f(M - n), fb = exp2f(mi - n);
+        const float n = fmaxf(M, mi), fa = ex2(M - n), fb = ex2(mi - n);
         acc = acc * fa + x * fb;
         l = l * fa + li * fb;
         M = n;
@@ -867,14 +867,14 @@ __global__ void __launch_bounds__(32 * kKv8Warps) kv8_join_kernel(Kv8AttnArgs a,
     __syncthreads();
     if (half == 0) {
         const int i = threadIdx.x & 127;
-        const float n = fmaxf(M, sh[0][i]), fa = exp2f(M - n), fb = exp2f(sh[0][i] - n);
+        const float n = fmaxf(M, sh[0][i]), fa = ex2(M - n), fb = ex2(sh[0][i] - n);
         kv8_store(a, orow, dim, acc * fa + sh[2][i] * fb, n, l * fa + sh[1][i] * fb);
     }
 }
 
 // ------------------------------------------------------------- host side
 
-constexpr int kKv8Least = 16;  // tiles a CTA takes at least: two a warp
+constexpr int kKv8Least = 8;  // chunks a CTA takes at least: one a warp
 
 template <int NT>
 static int kv8_ctas() { return num_sms() * (NT == 1 ? 2 : 1); }
@@ -888,7 +888,7 @@ static size_t kv8_ws_bytes() { return (size_t)kv8_ctas<NT>() * 2 * kv8_part_floa
 template <int FMT, int NT, bool LIST>
 static lsa_status launch_kv8_split(const Kv8AttnArgs& a, cudaStream_t st) {
     const int n = kv8_ctas<NT>();
-    const size_t smem = (size_t)kKv8Warps * 8 * NT * (kKv8Pad + 2) * sizeof(float);
+    const size_t smem = (size_t)kKv8Warps * kKv8Ring;
     cudaFuncSetAttribute(kv8_split_kernel<FMT, NT, LIST>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     lsa_status s;
     {
@@ -998,9 +998,11 @@ lsa_status lsa_kv8_sparse_attn(const lsa_kv8* kv, const uint16_t* Q, int64_t q_s
         return kv->fmt == LSA_KV8_E4M3 ? launch_kv8_split<0, 1, true>(a, st) : launch_kv8_split<1, 1, true>(a, st);
     {
         KTime kt_("kv8_list_kernel", st);
-        const unsigned grid = (unsigned)ceil_div<int64_t>(nq * kv->hkv, kKv8Warps);
-        if (kv->fmt == LSA_KV8_E4M3) kv8_list_kernel<0><<<grid, 32 * kKv8Warps, 0, st>>>(a);
-        else kv8_list_kernel<1><<<grid, 32 * kKv8Warps, 0, st>>>(a);
+        const unsigned grid = (unsigned)ceil_div<int64_t>(nq * kv->hkv, kKv8ListWarps);
+        auto kern = kv->fmt == LSA_KV8_E4M3 ? kv8_list_kernel<0> : kv8_list_kernel<1>;
+        const int smem = kKv8ListWarps * kKv8Ring;
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        kern<<<grid, 32 * kKv8ListWarps, smem, st>>>(a);
     }
     return check_launch("kv8_list_kernel");
 }

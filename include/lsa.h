@@ -605,7 +605,7 @@ lsa_status lsa_lse_combine(const float* O_parts, const float* lse_parts, int32_t
  * A page number outside the pool, or a token range outside the table, raises
  * the device error word (LSA_EDEVICE at the next lsa_check_device_error) and
  * the rows concerned are skipped.  page is 16, 32, 64, 128 or 256; n_pages *
- * hkv * page < 2^31; K and V 16-byte aligned, scale 8-byte.
+ * hkv * page < 2^31; K and V 128-byte aligned, scale 8-byte.
  */
 #define LSA_KV8_E4M3 0
 #define LSA_KV8_INT8 1
