@@ -126,10 +126,10 @@ def lib():
         L.lsa_lse_combine.argtypes = [vp, vp, i32, i64, i32, vp, vp]
         L.lsa_attn_backward.argtypes = [vp, vp, vp, vp, vp, vp, i64, i32, i32, i32, i64, vp, vp, vp, vp]
         L.lsa_kv8_write.argtypes = [P(lsa_kv8), vp, i64, vp, i64, i64, vp, vp, vp, i32, i32, vp]
-        L.lsa_kv8_attn_workspace_bytes.argtypes = [i64, i32, i32, i32]
+        L.lsa_kv8_attn_workspace_bytes.argtypes = [P(lsa_kv8), i64, i32, i32, i32, i32, i32, i32]
         L.lsa_kv8_attn_workspace_bytes.restype = sz
         L.lsa_kv8_attn.argtypes = [P(lsa_kv8), vp, i64, i64, i32, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, sz, vp]
-        L.lsa_kv8_sparse_attn_workspace_bytes.argtypes = [i64, i32, i32]
+        L.lsa_kv8_sparse_attn_workspace_bytes.argtypes = [P(lsa_kv8), i64, i32, i32]
         L.lsa_kv8_sparse_attn_workspace_bytes.restype = sz
         L.lsa_kv8_sparse_attn.argtypes = [P(lsa_kv8), vp, i64, i64, i32, vp, vp, vp, i32, i32, vp, i32, vp, vp, vp, sz, vp]
         L.lsa_kv8_copy_pages.argtypes = [P(lsa_kv8), vp, vp, i64, vp]

@@ -37,10 +37,16 @@ def _spec(t, name, dtype, shape=None):
         return
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if shape is not None and (t.dim() != len(shape) or
-                              any(n is not None and t.shape[i] != n for i, n in enumerate(shape))):
-        want = tuple("*" if n is None else n for n in shape)
-        raise ValueError(f"{name}: expected shape {want}, got {tuple(t.shape)}")
+    if shape is None or t.shape == shape:
+        return
+    if len(t.shape) == len(shape):
+        for n, m in zip(shape, t.shape):
+            if n is not None and n != m:
+                break
+        else:
+            return
+    want = tuple("*" if n is None else n for n in shape)
+    raise ValueError(f"{name}: expected shape {want}, got {tuple(t.shape)}")
 
 
 def _need_cuda(*ts):
@@ -553,6 +559,7 @@ def lse_combine(O_parts, lse_parts, O=None, stream=None) -> torch.Tensor:
 # ------------------------------------------------ paged 8-bit K/V cache
 
 KV8_DTYPES = {"e4m3": torch.float8_e4m3fn, "int8": torch.int8}
+KV8_FMT = {torch.float8_e4m3fn: 0, torch.int8: 1}
 KV8_PAGES = (16, 32, 64, 128, 256)
 
 
@@ -575,45 +582,29 @@ class KV8:
     @classmethod
     def of(cls, K: torch.Tensor, V: torch.Tensor, scale: torch.Tensor) -> "KV8":
         """A cache over arrays the caller holds."""
-        if K.dtype not in KV8_DTYPES.values():
-            raise TypeError(f"K: expected one of {tuple(KV8_DTYPES.values())}, got {K.dtype}")
-        _spec(K, "K", K.dtype, (None, None, None, 128))
-        _spec(V, "V", K.dtype, tuple(K.shape))
-        _spec(scale, "scale", F32, (K.shape[0], K.shape[1], 2))
-        if K.shape[2] not in KV8_PAGES:
-            raise ValueError(f"page: expected one of {KV8_PAGES}, got {K.shape[2]}")
+        if K.dtype not in KV8_FMT:
+            raise TypeError(f"K: expected one of {tuple(KV8_FMT)}, got {K.dtype}")
+        if K.dim() != 4 or K.shape[3] != 128:
+            raise ValueError(f"K: expected shape ('*', '*', '*', 128), got {tuple(K.shape)}")
+        n_pages, hkv, page, _ = K.shape
+        _spec(V, "V", K.dtype, K.shape)
+        _spec(scale, "scale", F32, (n_pages, hkv, 2))
+        if page not in KV8_PAGES:
+            raise ValueError(f"page: expected one of {KV8_PAGES}, got {page}")
         _need_cuda(K, V, scale)
+        _on(K.device, V, scale)
         kv = cls.__new__(cls)
         kv._wrap(K, V, scale)
         return kv
 
     def _wrap(self, K, V, scale):
         self.K, self.V, self.scale = K, V, scale
-        self.n_pages, self.hkv, self.page = int(K.shape[0]), int(K.shape[1]), int(K.shape[2])
-        self.fmt = "e4m3" if K.dtype == torch.float8_e4m3fn else "int8"
+        self.n_pages, self.hkv, self.page, _ = K.shape
+        code = KV8_FMT[K.dtype]
+        self.fmt = "int8" if code else "e4m3"
         self.device = K.device
-        self.c = _lib.lsa_kv8(0 if self.fmt == "e4m3" else 1, self.hkv, self.page, self.n_pages, K.data_ptr(),
-                              V.data_ptr(), scale.data_ptr())
+        self.c = _lib.lsa_kv8(code, self.hkv, self.page, self.n_pages, K.data_ptr(), V.data_ptr(), scale.data_ptr())
         self._ref = ctypes.byref(self.c)
-
-
-def _rows(t, name, heads):
-    """Elements between the token rows of a bf16 [n, heads, 128] tensor whose
-    rows are dense (its token stride may be larger: a slice of a fused
-    projection)."""
-    _spec(t, name, BF16, (None, heads, 128))
-    if not t.is_cuda:
-        raise ValueError("LSA calls take CUDA tensors (there is no CPU implementation)")
-    n, dense = t.shape[0], t.shape[1] * 128
-    if n <= 1:
-        ld = dense
-        ok = t.shape[1] <= 1 or t.stride(1) == 128
-    else:
-        ld = t.stride(0)
-        ok = (t.shape[1] <= 1 or t.stride(1) == 128) and ld >= dense and ld % 8 == 0
-    if not ok or t.stride(2) != 1:
-        raise ValueError(f"{name}: token rows must be dense and a multiple of 8 elements apart, got strides {t.stride()}")
-    return ld
 
 
 def _on(dev, *ts):
@@ -622,40 +613,59 @@ def _on(dev, *ts):
             raise ValueError(f"LSA calls take tensors of one device: got {t.device} beside {dev}")
 
 
-class _KV8Call:
-    """The device and stream of one call: makes the cache's device current
-    while it launches, and keeps what the call allocated from reuse until
-    `stream` is done with it."""
-
-    def __init__(self, dev, stream):
-        self.dev, self.given, self.prev = dev, stream, None
-
-    def __enter__(self):
-        if torch.cuda.current_device() != self.dev.index:
-            self.prev = torch.cuda.device(self.dev)
-            self.prev.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        if self.prev is not None:
-            self.prev.__exit__(*exc)
-        return False
-
-    def new(self, shape, dtype):
-        t = torch.empty(shape, dtype=dtype, device=self.dev)
-        if self.given is not None:
-            t.record_stream(self.given)
-        return t
-
-    def stream(self):
-        s = self.given if self.given is not None else torch.cuda.current_stream(self.dev)
-        return ctypes.c_void_p(s.cuda_stream)
+def _arg(t, name, dtype, dev, shape):
+    """An argument's dtype, shape (None entries match any size) and layout: a
+    dense tensor on the cache's device.  Returns its address (None for None)."""
+    if t is None:
+        return None
+    _spec(t, name, dtype, shape)
+    if not t.is_cuda:
+        raise ValueError("LSA calls take CUDA tensors (there is no CPU implementation)")
+    if t.device != dev:
+        raise ValueError(f"LSA calls take tensors of one device: got {name} on {t.device} beside {dev}")
+    if not t.is_contiguous():
+        raise ValueError("LSA calls take contiguous tensors")
+    return t.data_ptr()
 
 
-def _table(kv, table, per_seq, name):
-    _spec(table, "table", I32, (None, None))
-    _spec(per_seq, name, I32, (table.shape[0],))
-    return int(table.shape[0]), int(table.shape[1])
+def _rows(t, name, heads, dev):
+    """A bf16 [n, heads, 128] tensor whose token rows are dense (their stride
+    may be larger: a slice of a fused projection).  Returns its address and the
+    elements between rows."""
+    if t.dtype != BF16 or t.dim() != 3 or t.shape[2] != 128 or (heads is not None and t.shape[1] != heads):
+        _spec(t, name, BF16, (None, heads, 128))
+    if not t.is_cuda:
+        raise ValueError("LSA calls take CUDA tensors (there is no CPU implementation)")
+    if t.device != dev:
+        raise ValueError(f"LSA calls take tensors of one device: got {name} on {t.device} beside {dev}")
+    n, h, _ = t.shape
+    dense = h * 128
+    if t.is_contiguous():
+        return t.data_ptr(), dense
+    ld, sh, sd = t.stride()
+    if n <= 1:
+        ld = dense
+    if sd != 1 or (h > 1 and sh != 128) or ld < dense or ld % 8:
+        raise ValueError(f"{name}: token rows must be dense and a multiple of 8 elements apart, got strides {t.stride()}")
+    return t.data_ptr(), ld
+
+
+def _launch(kv, stream, name, call, *made):
+    """Run `call(stream handle)` with the cache's device current.  What the
+    call allocated (`made`) is kept from reuse until `stream` is done with it."""
+    dev = kv.device
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return _launch(kv, stream, name, call, *made)
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(dev.index)
+    else:
+        handle = stream.cuda_stream
+        for t in made:
+            t.record_stream(stream)
+    status = call(handle)
+    if status:
+        check(status, name)
 
 
 def kv8_write(kv: KV8, K: torch.Tensor, V: torch.Tensor, table: torch.Tensor, start: torch.Tensor, cu=None,
@@ -663,38 +673,51 @@ def kv8_write(kv: KV8, K: torch.Tensor, V: torch.Tensor, table: torch.Tensor, st
     """lsa_kv8_write: new tokens' K/V rows [n, hkv, 128] bf16 into the pages of
     their sequences: sequence b's rows cu[b] .. cu[b + 1] - 1 (cu None: one
     token each) at positions start[b] on, in pages table[b]."""
-    n_seq, max_pages = _table(kv, table, start, "start")
-    ldk, ldv = _rows(K, "K", kv.hkv), _rows(V, "V", kv.hkv)
-    n = int(K.shape[0])
-    _spec(V, "V", BF16, tuple(K.shape))
-    _spec(cu, "cu", I32, (n_seq + 1,))
+    dev = kv.device
+    pk, ldk = _rows(K, "K", kv.hkv, dev)
+    pv, ldv = _rows(V, "V", kv.hkv, dev)
+    n = K.shape[0]
+    if V.shape[0] != n:
+        raise ValueError(f"V: expected shape {tuple(K.shape)}, got {tuple(V.shape)}")
+    pt = _arg(table, "table", I32, dev, (None, None))
+    n_seq, max_pages = table.shape
+    ps = _arg(start, "start", I32, dev, (n_seq,))
+    pc = _arg(cu, "cu", I32, dev, (n_seq + 1,))
     if cu is None and n != n_seq:
         raise ValueError(f"K: without cu, expected one row for each of {n_seq} sequences, got {n}")
-    _need_cuda(table, start, cu)
-    _on(kv.device, K, V, table, start, cu)
-    with _KV8Call(kv.device, stream) as call:
-        check(lib().lsa_kv8_write(kv._ref, _ptr(K), ldk, _ptr(V), ldv, n, _ptr(cu), _ptr(start), _ptr(table), n_seq,
-                                  max_pages, call.stream()), "lsa_kv8_write")
+    _launch(kv, stream, "lsa_kv8_write",
+            lambda s: lib().lsa_kv8_write(kv._ref, pk, ldk, pv, ldv, n, pc, ps, pt, n_seq, max_pages, s))
     return kv
 
 
-def kv8_attn_workspace_bytes(nq: int, n_seq: int, hq: int, hkv: int) -> int:
-    return int(lib().lsa_kv8_attn_workspace_bytes(nq, n_seq, hq, hkv))
+def kv8_attn_workspace_bytes(kv: KV8, nq: int, hq: int, n_seq: int, max_pages: int, one_each: bool = True,
+                             sinks: int = 0, window: int = 0) -> int:
+    """Bytes of `ws` that kv8_attn needs (0: none) for nq queries of n_seq
+    sequences with tables of max_pages; one_each: called without cu."""
+    return int(lib().lsa_kv8_attn_workspace_bytes(kv._ref, nq, hq, one_each, n_seq, max_pages, sinks, window))
 
 
-def kv8_sparse_attn_workspace_bytes(nq: int, hq: int, hkv: int) -> int:
-    return int(lib().lsa_kv8_sparse_attn_workspace_bytes(nq, hq, hkv))
+def kv8_sparse_attn_workspace_bytes(kv: KV8, nq: int, hq: int, n_idx: int) -> int:
+    """Bytes of `ws` that kv8_sparse_attn needs (0: none) for lists of n_idx."""
+    return int(lib().lsa_kv8_sparse_attn_workspace_bytes(kv._ref, nq, hq, n_idx))
 
 
-def _kv8_out(call, Q, O, lse, ws, need):
-    nq, hq = int(Q.shape[0]), int(Q.shape[1])
+def _kv8_buffers(dev, nq, hq, O, lse, ws, need):
+    """O, lse and ws, allocated where the caller gave none (or too small a ws),
+    their addresses, and what was allocated."""
+    made = []
     if O is None:
-        O = call.new((nq, hq, 128), BF16)
+        O = torch.empty((nq, hq, 128), dtype=BF16, device=dev)
+        made.append(O)
     if lse is None:
-        lse = call.new((nq, hq), F32)
+        lse = torch.empty((nq, hq), dtype=F32, device=dev)
+        made.append(lse)
     if ws is None or ws.numel() < need:
-        ws = call.new((max(need, 1),), torch.uint8)
-    return O, lse, ws
+        ws = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
+        if need:
+            made.append(ws)
+    return (O, lse, O.data_ptr(), lse.data_ptr(), None if ws is None else ws.data_ptr(),
+            0 if ws is None else ws.numel(), made)
 
 
 def kv8_attn(Q: torch.Tensor, kv: KV8, table: torch.Tensor, lens: torch.Tensor, cu=None, sinks: int = 0,
@@ -704,22 +727,24 @@ def kv8_attn(Q: torch.Tensor, kv: KV8, table: torch.Tensor, lens: torch.Tensor, 
     `sinks`).  Q [nq, hq, 128] bf16, sequence b's rows cu[b] .. cu[b + 1] - 1
     (cu None: one each); lens counts the new tokens too.  Returns (O bf16
     [nq, hq, 128], lse fp32 [nq, hq], base 2)."""
-    n_seq, max_pages = _table(kv, table, lens, "lens")
-    ld = _rows(Q, "Q", None)
-    nq, hq = int(Q.shape[0]), int(Q.shape[1])
-    _spec(cu, "cu", I32, (n_seq + 1,))
-    _spec(O, "O", BF16, (nq, hq, 128))
-    _spec(lse, "lse", F32, (nq, hq))
-    _spec(ws, "ws", torch.uint8, (None,))
+    dev, L = kv.device, lib()
+    pq, ld = _rows(Q, "Q", None, dev)
+    nq, hq, _ = Q.shape
+    pt = _arg(table, "table", I32, dev, (None, None))
+    n_seq, max_pages = table.shape
+    pl = _arg(lens, "lens", I32, dev, (n_seq,))
+    pc = _arg(cu, "cu", I32, dev, (n_seq + 1,))
+    _arg(O, "O", BF16, dev, (nq, hq, 128))
+    _arg(lse, "lse", F32, dev, (nq, hq))
+    _arg(ws, "ws", torch.uint8, dev, (None,))
     if cu is None and nq != n_seq:
         raise ValueError(f"Q: without cu, expected one row for each of {n_seq} sequences, got {nq}")
-    _need_cuda(table, lens, cu, O, lse, ws)
-    _on(kv.device, Q, table, lens, cu, O, lse, ws)
-    with _KV8Call(kv.device, stream) as call:
-        O, lse, ws = _kv8_out(call, Q, O, lse, ws, kv8_attn_workspace_bytes(nq, n_seq, hq, kv.hkv))
-        check(lib().lsa_kv8_attn(kv._ref, _ptr(Q), ld, nq, hq, _ptr(cu), _ptr(table), _ptr(lens), n_seq, max_pages,
-                                 sinks, window, _ptr(O), _ptr(lse), _ptr(ws), ws.numel(), call.stream()),
-              "lsa_kv8_attn")
+    O, lse, po, pe, pw, nw, made = _kv8_buffers(dev, nq, hq, O, lse, ws,
+                                                L.lsa_kv8_attn_workspace_bytes(kv._ref, nq, hq, cu is None, n_seq, max_pages,
+                                                                               sinks, window))
+    _launch(kv, stream, "lsa_kv8_attn",
+            lambda s: L.lsa_kv8_attn(kv._ref, pq, ld, nq, hq, pc, pt, pl, n_seq, max_pages, sinks, window, po, pe, pw,
+                                     nw, s), *made)
     return O, lse
 
 
@@ -729,38 +754,44 @@ def kv8_sparse_attn(Q: torch.Tensor, kv: KV8, table: torch.Tensor, lens: torch.T
     idx [nq, hkv, n_idx] int32 positions in the query's sequence seq[i] (seq
     None: query i is sequence i's), -1 = padding.  Returns (O bf16
     [nq, hq, 128], lse fp32 [nq, hq], base 2)."""
-    n_seq, max_pages = _table(kv, table, lens, "lens")
-    ld = _rows(Q, "Q", None)
-    nq, hq = int(Q.shape[0]), int(Q.shape[1])
-    _spec(idx, "idx", I32, (nq, kv.hkv, None))
-    _spec(seq, "seq", I32, (nq,))
-    _spec(O, "O", BF16, (nq, hq, 128))
-    _spec(lse, "lse", F32, (nq, hq))
-    _spec(ws, "ws", torch.uint8, (None,))
+    dev, L = kv.device, lib()
+    pq, ld = _rows(Q, "Q", None, dev)
+    nq, hq, _ = Q.shape
+    pt = _arg(table, "table", I32, dev, (None, None))
+    n_seq, max_pages = table.shape
+    pl = _arg(lens, "lens", I32, dev, (n_seq,))
+    pi = _arg(idx, "idx", I32, dev, (nq, kv.hkv, None))
+    pb = _arg(seq, "seq", I32, dev, (nq,))
+    _arg(O, "O", BF16, dev, (nq, hq, 128))
+    _arg(lse, "lse", F32, dev, (nq, hq))
+    _arg(ws, "ws", torch.uint8, dev, (None,))
     if seq is None and nq != n_seq:
         raise ValueError(f"Q: without seq, expected one row for each of {n_seq} sequences, got {nq}")
-    _need_cuda(table, lens, idx, seq, O, lse, ws)
-    _on(kv.device, Q, table, lens, idx, seq, O, lse, ws)
-    with _KV8Call(kv.device, stream) as call:
-        O, lse, ws = _kv8_out(call, Q, O, lse, ws, kv8_sparse_attn_workspace_bytes(nq, hq, kv.hkv))
-        check(lib().lsa_kv8_sparse_attn(kv._ref, _ptr(Q), ld, nq, hq, _ptr(seq), _ptr(table), _ptr(lens), n_seq,
-                                        max_pages, _ptr(idx), idx.shape[2], _ptr(O), _ptr(lse), _ptr(ws), ws.numel(),
-                                        call.stream()), "lsa_kv8_sparse_attn")
+    n_idx = idx.shape[2]
+    O, lse, po, pe, pw, nw, made = _kv8_buffers(dev, nq, hq, O, lse, ws,
+                                                L.lsa_kv8_sparse_attn_workspace_bytes(kv._ref, nq, hq, n_idx))
+    _launch(kv, stream, "lsa_kv8_sparse_attn",
+            lambda s: L.lsa_kv8_sparse_attn(kv._ref, pq, ld, nq, hq, pb, pt, pl, n_seq, max_pages, pi, n_idx, po, pe,
+                                            pw, nw, s), *made)
     return O, lse
 
 
 def kv8_copy_pages(kv: KV8, src, dst, stream=None) -> KV8:
     """lsa_kv8_copy_pages: page src[i] onto page dst[i] (host sequences of page
     numbers; no page may be written twice, or both read and written)."""
-    src, dst = (np.ascontiguousarray(x, dtype=np.int64) for x in (src, dst))
-    if src.ndim != 1 or src.shape != dst.shape:
-        raise ValueError(f"src and dst: expected two lists of one length, got shapes {src.shape} and {dst.shape}")
-    if src.size and max(src.max(), dst.max()) >= kv.n_pages or src.size and min(src.min(), dst.min()) < 0:
-        raise ValueError(f"src and dst: page numbers must be in [0, {kv.n_pages})")
-    src, dst = src.astype(np.int32), dst.astype(np.int32)
-    with _KV8Call(kv.device, stream) as call:
-        check(lib().lsa_kv8_copy_pages(kv._ref, src.ctypes.data_as(ctypes.c_void_p), dst.ctypes.data_as(ctypes.c_void_p),
-                                       src.size, call.stream()), "lsa_kv8_copy_pages")
+    pair = []
+    for name, x in (("src", src), ("dst", dst)):
+        x = np.asarray(x)
+        if x.ndim != 1 or (x.size and x.dtype.kind not in "iu"):
+            raise ValueError(f"{name}: expected a list of page numbers, got shape {x.shape} of {x.dtype}")
+        if x.dtype != np.int32 and x.size and (x.min() < 0 or x.max() >= kv.n_pages):
+            raise ValueError(f"{name}: page numbers must be in [0, {kv.n_pages})")
+        pair.append(np.ascontiguousarray(x, dtype=np.int32))
+    src, dst = pair
+    if src.size != dst.size:
+        raise ValueError(f"src and dst: expected two lists of one length, got {src.size} and {dst.size}")
+    ps, pd, n = src.__array_interface__["data"][0], dst.__array_interface__["data"][0], src.size
+    _launch(kv, stream, "lsa_kv8_copy_pages", lambda s: lib().lsa_kv8_copy_pages(kv._ref, ps, pd, n, s))
     return kv
 
 

@@ -55,6 +55,7 @@ struct Kv8AttnArgs {
     uint16_t* O;           // [nq, hq, 128]
     float* lse;            // [nq, hq] or NULL
     float* part;           // split rows' partial states
+    int32_t rows_per_seq;  // > 0: a CTA for each row, so many for each sequence
     float scale_log2;
 };
 
@@ -581,6 +582,8 @@ __global__ void __launch_bounds__(32 * kKv8ListWarps, 2) kv8_list_kernel(Kv8Attn
 // that crosses CTAs leaves a partial state in every CTA it touches (slot 0 if
 // it began before the CTA, slot 1 if it began inside), and kv8_join_kernel
 // joins them.  Everyone derives the stream from lens and cu by the same scan.
+// Where the call's shapes alone say that every row is short, each row gets a
+// CTA of its own instead (rows_per_seq > 0): no scan, no second kernel.
 struct Kv8Seq {
     int64_t base;     // first chunk of the sequence in the stream
     int32_t chunks;   // chunks of each of its rows
@@ -620,82 +623,82 @@ __device__ __forceinline__ void kv8_seq(const Kv8AttnArgs& a, int64_t b, Kv8Seq&
     }
 }
 
+// Sum of v over the CTA's threads before this one, and over all of them.
+__device__ __forceinline__ long long kv8_block_scan(long long v, long long& all) {
+    __shared__ long long wsum[kKv8Warps];
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    long long inc = v;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const long long up = __shfl_up_sync(0xffffffffu, inc, off);
+        if (lane >= off) inc += up;
+    }
+    if (lane == 31) wsum[wid] = inc;
+    __syncthreads();
+    long long before = inc - v;
+    all = 0;
+#pragma unroll
+    for (int i = 0; i < kKv8Warps; ++i) {
+        if (i < wid) before += wsum[i];
+        all += wsum[i];
+    }
+    __syncthreads();
+    return before;
+}
+
 template <int NT, bool LIST>
 struct Kv8Scan {
     int64_t total, per;
-    // Chunks of all sequences, and each CTA's share of them.  `least`: chunks a
-    // CTA takes at least.
+    long long begin, count, round;  // this thread's sequence in the first round of 256: its place, its chunks; the round's
+
+    __device__ __forceinline__ long long chunks_of(const Kv8AttnArgs& a, int64_t b) const {
+        if (b >= a.n_seq) return 0;
+        Kv8Seq q;
+        kv8_seq<NT, LIST>(a, b, q);
+        return (int64_t)q.chunks * q.rows;
+    }
+    // Chunks of all sequences and each CTA's share of them (`least`: chunks a
+    // CTA takes at least).
     __device__ __forceinline__ void init(const Kv8AttnArgs& a, int n_cta, int least) {
         if constexpr (LIST) {
-            Kv8Seq q;
-            kv8_seq<NT, true>(a, 0, q);
-            total = a.nq * a.hkv * (int64_t)q.chunks;
+            total = a.nq * a.hkv * (int64_t)max(1, (a.n_idx + 31) / 32);
         } else {
-            __shared__ long long sum[kKv8Warps];
-            long long mine = 0;
-            for (int64_t b = threadIdx.x; b < a.n_seq; b += 32 * kKv8Warps) {
-                Kv8Seq q;
-                kv8_seq<NT, false>(a, b, q);
-                mine += (int64_t)q.chunks * q.rows;
+            count = chunks_of(a, threadIdx.x);
+            begin = kv8_block_scan(count, round);
+            total = round;
+            for (int64_t b0 = 32 * kKv8Warps; b0 < a.n_seq; b0 += 32 * kKv8Warps) {
+                long long all;
+                kv8_block_scan(chunks_of(a, b0 + threadIdx.x), all);
+                total += all;
             }
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, off);
-            if ((threadIdx.x & 31) == 0) sum[threadIdx.x >> 5] = mine;
-            __syncthreads();
-            total = 0;
-#pragma unroll
-            for (int i = 0; i < kKv8Warps; ++i) total += sum[i];
-            __syncthreads();
         }
         per = max((int64_t)least, (total + n_cta - 1) / n_cta);
     }
     // The sequence whose chunks hold position w of the stream (0 <= w < total).
     __device__ __forceinline__ int64_t find(const Kv8AttnArgs& a, int64_t w, Kv8Seq& out) {
+        int64_t b, base;
         if constexpr (LIST) {
-            kv8_seq<NT, true>(a, 0, out);
-            const int64_t b = w / ((int64_t)out.chunks * out.rows);
-            kv8_seq<NT, true>(a, b, out);
-            out.base = b * out.chunks * out.rows;
-            return b;
+            b = w / (total / a.nq);
+            base = b * (total / a.nq);
         } else {
-            __shared__ long long wsum[kKv8Warps];
-            __shared__ long long fb, fbase;
-            const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-            long long base = 0;
-            for (int64_t b0 = 0; b0 < a.n_seq; b0 += 32 * kKv8Warps) {
-                const int64_t b = b0 + threadIdx.x;
-                long long m = 0;
-                if (b < a.n_seq) {
-                    Kv8Seq q;
-                    kv8_seq<NT, false>(a, b, q);
-                    m = (int64_t)q.chunks * q.rows;
-                }
-                long long inc = m;
-#pragma unroll
-                for (int off = 1; off < 32; off <<= 1) {
-                    const long long up = __shfl_up_sync(0xffffffffu, inc, off);
-                    if (lane >= off) inc += up;
-                }
-                if (lane == 31) wsum[wid] = inc;
-                __syncthreads();
-                long long before = base, all = base;
-#pragma unroll
-                for (int i = 0; i < kKv8Warps; ++i) {
-                    if (i < wid) before += wsum[i];
-                    all += wsum[i];
-                }
-                const long long first = before + inc - m;
-                if (w >= first && w < first + m) { fb = b; fbase = first; }
-                __syncthreads();
-                base = all;
-                if (w < base) break;  // uniform: every thread holds the same sums
+            __shared__ long long found[2];
+            long long first = begin, m = count, end = round;
+            b = threadIdx.x;
+            while (w >= end) {  // uniform
+                long long all;
+                b += 32 * kKv8Warps;
+                m = chunks_of(a, b);
+                first = end + kv8_block_scan(m, all);
+                end += all;
             }
-            const int64_t b = fb;
-            kv8_seq<NT, false>(a, b, out);
-            out.base = fbase;
+            if (w >= first && w < first + m) { found[0] = b; found[1] = first; }
             __syncthreads();
-            return b;
+            b = found[0];
+            base = found[1];
         }
+        kv8_seq<NT, LIST>(a, b, out);
+        out.base = base;
+        return b;
     }
 };
 
@@ -727,12 +730,25 @@ __global__ void __launch_bounds__(32 * kKv8Warps, NT == 1 ? 2 : 1) kv8_split_ker
     // a warp's sums go where its ring was: [8 NT][kKv8Pad] floats
     auto so = [&](int w) { return reinterpret_cast<float*>(ksm + w * kKv8Ring); };
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, gq = lane >> 2, tq = lane & 3;
-    Kv8Scan<NT, LIST> scan;
-    scan.init(a, (int)gridDim.x, least);
-    const int64_t w0 = (int64_t)blockIdx.x * scan.per, w1 = min(scan.total, w0 + scan.per);
-    if (w0 >= w1) return;
     Kv8Seq q;
-    int64_t b = scan.find(a, w0, q);
+    int64_t b, w0, w1;
+    if (a.rows_per_seq > 0) {  // a CTA for each row
+        b = blockIdx.x / a.rows_per_seq;
+        const int r = blockIdx.x % a.rows_per_seq;
+        kv8_seq<NT, LIST>(a, b, q);
+        if (r >= q.rows) return;
+        q.base = 0;
+        w0 = (int64_t)r * q.chunks;
+        w1 = w0 + q.chunks;
+    } else {
+        asm volatile("griddepcontrol.launch_dependents;\n");
+        Kv8Scan<NT, LIST> scan;
+        scan.init(a, (int)gridDim.x, least);
+        w0 = (int64_t)blockIdx.x * scan.per;
+        w1 = min(scan.total, w0 + scan.per);
+        if (w0 >= w1) return;
+        b = scan.find(a, w0, q);
+    }
     for (int64_t w = w0; w < w1;) {
         while (w >= q.base + (int64_t)q.chunks * q.rows) {  // the next sequence that has rows
             const int64_t next = q.base + (int64_t)q.chunks * q.rows;
@@ -830,51 +846,63 @@ __global__ void __launch_bounds__(32 * kKv8Warps, NT == 1 ? 2 : 1) kv8_split_ker
     }
 }
 
-// Joins the partial states of the row that crosses the end of CTA c's range,
-// if that row began inside it.  blockIdx.y: an eighth of the columns' sums.
+// Joins one column (blockIdx.y) of the row that crosses the end of CTA c's
+// range, if that row began inside it: every warp takes each eighth state, a
+// lane four of its sums.
 template <int NT, bool LIST>
 __global__ void __launch_bounds__(32 * kKv8Warps) kv8_join_kernel(Kv8AttnArgs a, int n_cta, int least) {
     Kv8Scan<NT, LIST> scan;
     scan.init(a, n_cta, least);
     const int64_t c = blockIdx.x, w0 = c * scan.per, w1 = w0 + scan.per;
+    Kv8Seq q{};
+    if (w1 < scan.total) scan.find(a, w1, q);
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");  // before any exit: this grid's end is the call's end
     if (w1 >= scan.total) return;
-    Kv8Seq q;
-    scan.find(a, w1, q);
-    const int64_t r = (w1 - q.base) / q.chunks;
-    const int64_t begin = q.base + r * q.chunks, end = begin + q.chunks;
-    if (begin == w1 || begin < w0) return;
-    const int g = (int)(r / q.groups), cg = (int)(r % q.groups);
-    const int more = (int)((end - 1) / scan.per - c);  // CTAs after c that hold chunks of the row
-    const int e = blockIdx.y * 128 + (threadIdx.x & 127), half = threadIdx.x >> 7;
-    const int col = e / kD, dim = e % kD;
-    const int64_t orow = kv8_out_row<NT>(a, q, cg, g, col);
-    if (orow < 0) return;
-    const int64_t stride = 2 * kv8_part_floats<NT>();
-    const float* first = a.part + (2 * c + 1) * kv8_part_floats<NT>();
-    const float* rest = a.part + 2 * (c + 1) * kv8_part_floats<NT>();
-    __shared__ float sh[3][128];
-    auto at = [&](int i) { return i == 0 ? first : rest + (int64_t)(i - 1) * stride; };
-    float M = -FLT_MAX, l = 0.f, acc = 0.f;
-    for (int i = half; i <= more; i += 2) {
-        const float* p = at(i);
-        const float mi = p[8 * NT * kD + 2 * col], li = p[8 * NT * kD + 2 * col + 1], x = p[col * kD + dim];
-        const float n = fmaxf(M, mi), fa = ex2(M - n), fb = ex2(mi - n);
-        acc = acc * fa + x * fb;
-        l = l * fa + li * fb;
-        M = n;
+    const int r = (int)((w1 - q.base) / q.chunks);
+    const int64_t begin = q.base + (int64_t)r * q.chunks, end = begin + q.chunks;
+    const int64_t orow = kv8_out_row<NT>(a, q, r % q.groups, r / q.groups, blockIdx.y);
+    if (begin == w1 || begin < w0 || orow < 0) return;
+    const int n = (int)((end - 1) / scan.per - c) + 1;  // states: CTA c's slot 1, the following CTAs' slots 0
+    __shared__ float4 s_acc[kKv8Warps][32];
+    __shared__ float2 s_ml[kKv8Warps];
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, col = blockIdx.y;
+    constexpr int kPart = kv8_part_floats<NT>();
+    float M = -FLT_MAX, l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = wid; i < n; i += kKv8Warps) {
+        const float* p = a.part + (2 * (c + i) + (i == 0)) * kPart;
+        const float2 ml = *reinterpret_cast<const float2*>(p + 8 * NT * kD + 2 * col);
+        const float4 x = *reinterpret_cast<const float4*>(p + col * kD + 4 * lane);
+        const float m = fmaxf(M, ml.x), fa = ex2(M - m), fb = ex2(ml.x - m);
+        acc = make_float4(acc.x * fa + x.x * fb, acc.y * fa + x.y * fb, acc.z * fa + x.z * fb, acc.w * fa + x.w * fb);
+        l = l * fa + ml.y * fb;
+        M = m;
     }
-    if (half == 1) { sh[0][threadIdx.x & 127] = M; sh[1][threadIdx.x & 127] = l; sh[2][threadIdx.x & 127] = acc; }
+    s_acc[wid][lane] = acc;
+    if (lane == 0) s_ml[wid] = make_float2(M, l);
     __syncthreads();
-    if (half == 0) {
-        const int i = threadIdx.x & 127;
-        const float n = fmaxf(M, sh[0][i]), fa = ex2(M - n), fb = ex2(sh[0][i] - n);
-        kv8_store(a, orow, dim, acc * fa + sh[2][i] * fb, n, l * fa + sh[1][i] * fb);
+    if (threadIdx.x >= kD) return;
+    const int dim = threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < kKv8Warps; ++i) M = i == 0 ? s_ml[0].x : fmaxf(M, s_ml[i].x);
+    float sum = 0.f;
+    l = 0.f;
+#pragma unroll
+    for (int i = 0; i < kKv8Warps; ++i) {
+        const float f = ex2(s_ml[i].x - M);
+        l += s_ml[i].y * f;
+        sum += reinterpret_cast<const float*>(s_acc[i])[dim] * f;
     }
+    kv8_store(a, orow, dim, sum, M, l);
 }
 
 // ------------------------------------------------------------- host side
 
-constexpr int kKv8Least = 8;  // chunks a CTA takes at least: one a warp
+// Chunks a CTA of the stream takes at least (one a warp), and chunks a row may
+// have for a CTA of its own (six a warp).
+constexpr int kKv8Least = 8;
+constexpr int kKv8Own = 48;
 
 template <int NT>
 static int kv8_ctas() { return num_sms() * (NT == 1 ? 2 : 1); }
@@ -882,12 +910,43 @@ static int kv8_ctas() { return num_sms() * (NT == 1 ? 2 : 1); }
 // Columns per warp step: 16 when a sequence has on average more than 8.
 static int kv8_nt(int64_t nq, int64_t n_seq, int G) { return nq * G > 8 * n_seq ? 2 : 1; }
 
-template <int NT>
-static size_t kv8_ws_bytes() { return (size_t)kv8_ctas<NT>() * 2 * kv8_part_floats<NT>() * sizeof(float); }
+// How a call's rows meet the GPU: one warp a row (lists only), one CTA a row
+// (n > 0 of them for each sequence), or the stream (n = 0).  It goes by what
+// the host knows: the numbers of rows and an upper bound of a row's chunks.
+struct Kv8Plan {
+    int nt;
+    bool warps;
+    int64_t rows_per_seq;
+    size_t ws;
+};
+
+static Kv8Plan kv8_plan(bool lists, int64_t nq, int64_t n_seq, int G, int32_t hkv, bool one_each, int64_t max_chunks) {
+    Kv8Plan p{};
+    p.nt = lists ? 1 : kv8_nt(nq, n_seq, G);
+    const int ctas = p.nt == 1 ? kv8_ctas<1>() : kv8_ctas<2>();
+    // lists: rows that fill the GPU twice with a warp each
+    p.warps = lists && nq * hkv >= (int64_t)ctas * kKv8Warps * 2;
+    if (p.warps) return p;
+    // one sequence can have all new tokens
+    const int64_t rows = hkv * (lists || one_each ? 1 : ceil_div<int64_t>(nq * G, 8 * p.nt));
+    // CTAs without a row exit at once, but not for free: at most four a CTA of the stream
+    if (max_chunks <= kKv8Own && rows * n_seq <= 4 * ctas) p.rows_per_seq = rows;
+    else p.ws = (size_t)ctas * 2 * (p.nt == 1 ? kv8_part_floats<1>() : kv8_part_floats<2>()) * sizeof(float);
+    return p;
+}
+
+// Chunks a dense row has at most.
+static int64_t kv8_max_chunks(int64_t nq, int32_t page, int32_t max_pages, int32_t sinks, int32_t window) {
+    const int64_t all = ceil_div<int64_t>((int64_t)max_pages * page, 32);
+    if (window <= 0) return all;
+    const int64_t some = ceil_div<int64_t>(sinks, 32) + ceil_div<int64_t>(nq + window, 32) + 1;
+    return some < all ? some : all;
+}
 
 template <int FMT, int NT, bool LIST>
-static lsa_status launch_kv8_split(const Kv8AttnArgs& a, cudaStream_t st) {
-    const int n = kv8_ctas<NT>();
+static lsa_status launch_kv8_split(Kv8AttnArgs a, const Kv8Plan& p, int64_t n_seq, bool one_each, cudaStream_t st) {
+    const int n = p.rows_per_seq > 0 ? (int)(p.rows_per_seq * n_seq) : kv8_ctas<NT>();
+    a.rows_per_seq = (int32_t)p.rows_per_seq;
     const size_t smem = (size_t)kKv8Warps * kKv8Ring;
     cudaFuncSetAttribute(kv8_split_kernel<FMT, NT, LIST>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     lsa_status s;
@@ -895,10 +954,20 @@ static lsa_status launch_kv8_split(const Kv8AttnArgs& a, cudaStream_t st) {
         KTime kt_("kv8_split_kernel", st);
         kv8_split_kernel<FMT, NT, LIST><<<n, 32 * kKv8Warps, smem, st>>>(a, kKv8Least);
     }
-    if ((s = check_launch("kv8_split_kernel")) != LSA_OK) return s;
+    if ((s = check_launch("kv8_split_kernel")) != LSA_OK || p.rows_per_seq > 0) return s;
+    // the join's own scan runs while the split kernel drains
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(n - 1, LIST || one_each ? a.G : 8 * NT);
+    cfg.blockDim = dim3(32 * kKv8Warps);
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
     {
         KTime kt_("kv8_join_kernel", st);
-        kv8_join_kernel<NT, LIST><<<dim3(n - 1, 8 * NT), 32 * kKv8Warps, 0, st>>>(a, n, kKv8Least);
+        cudaLaunchKernelEx(&cfg, kv8_join_kernel<NT, LIST>, a, n, kKv8Least);
     }
     return check_launch("kv8_join_kernel");
 }
@@ -935,17 +1004,16 @@ static Kv8AttnArgs kv8_args(const lsa_kv8* kv, const uint16_t* Q, int64_t q_stri
     return a;
 }
 
-// Lists: rows that fill the GPU with one warp each take the one-warp kernel.
-static bool kv8_many_rows(int64_t nq, int32_t hkv) { return nq * hkv >= (int64_t)num_sms() * 2 * kKv8Warps * 2; }
-
 }  // namespace lsa
 
 extern "C" {
 
-size_t lsa_kv8_attn_workspace_bytes(int64_t nq, int32_t n_seq, int32_t hq, int32_t hkv) {
+size_t lsa_kv8_attn_workspace_bytes(const lsa_kv8* kv, int64_t nq, int32_t hq, int32_t one_each, int32_t n_seq,
+                                    int32_t max_pages, int32_t sinks, int32_t window) {
     using namespace lsa;
-    if (nq <= 0 || n_seq <= 0 || check_heads(hq, hkv) != LSA_OK) return 0;
-    return kv8_nt(nq, n_seq, hq / hkv) == 1 ? kv8_ws_bytes<1>() : kv8_ws_bytes<2>();
+    if (check_kv8(kv) != LSA_OK || check_heads(hq, kv->hkv) != LSA_OK || nq <= 0 || n_seq <= 0 || max_pages < 0) return 0;
+    return kv8_plan(false, nq, n_seq, hq / kv->hkv, kv->hkv, one_each != 0,
+                    kv8_max_chunks(nq, kv->page, max_pages, sinks, window)).ws;
 }
 
 lsa_status lsa_kv8_attn(const lsa_kv8* kv, const uint16_t* Q, int64_t q_stride, int64_t nq, int32_t hq,
@@ -959,20 +1027,24 @@ lsa_status lsa_kv8_attn(const lsa_kv8* kv, const uint16_t* Q, int64_t q_stride, 
     if (sinks < 0 || window < 0) return set_error(LSA_EINVAL, "lsa_kv8_attn: need sinks >= 0 and window >= 0");
     if (!cu && nq != n_seq) return set_error(LSA_EINVAL, "lsa_kv8_attn: without cu, nq must equal n_seq");
     if (nq == 0) return LSA_OK;
-    if (!ws || ws_bytes < lsa_kv8_attn_workspace_bytes(nq, n_seq, hq, kv->hkv))
-        return set_error(LSA_ENOSPACE, "lsa_kv8_attn: workspace too small");
     Kv8AttnArgs a = kv8_args(kv, Q, q_stride, nq, hq, table, lens, n_seq, max_pages, O, lse, ws);
     a.cu = cu; a.S = window > 0 ? sinks : 0; a.W = window;
+    const Kv8Plan p = kv8_plan(false, nq, n_seq, a.G, kv->hkv, cu == nullptr,
+                               kv8_max_chunks(nq, kv->page, max_pages, sinks, window));
+    if (p.ws > 0 && (!ws || ws_bytes < p.ws)) return set_error(LSA_ENOSPACE, "lsa_kv8_attn: workspace too small");
     const cudaStream_t st = (cudaStream_t)stream;
-    const bool one = kv8_nt(nq, n_seq, a.G) == 1;
-    if (kv->fmt == LSA_KV8_E4M3) return one ? launch_kv8_split<0, 1, false>(a, st) : launch_kv8_split<0, 2, false>(a, st);
-    return one ? launch_kv8_split<1, 1, false>(a, st) : launch_kv8_split<1, 2, false>(a, st);
+    const bool each = cu == nullptr;
+    if (kv->fmt == LSA_KV8_E4M3)
+        return p.nt == 1 ? launch_kv8_split<0, 1, false>(a, p, n_seq, each, st)
+                         : launch_kv8_split<0, 2, false>(a, p, n_seq, each, st);
+    return p.nt == 1 ? launch_kv8_split<1, 1, false>(a, p, n_seq, each, st)
+                     : launch_kv8_split<1, 2, false>(a, p, n_seq, each, st);
 }
 
-size_t lsa_kv8_sparse_attn_workspace_bytes(int64_t nq, int32_t hq, int32_t hkv) {
+size_t lsa_kv8_sparse_attn_workspace_bytes(const lsa_kv8* kv, int64_t nq, int32_t hq, int32_t n_idx) {
     using namespace lsa;
-    if (nq <= 0 || check_heads(hq, hkv) != LSA_OK || kv8_many_rows(nq, hkv)) return 0;
-    return kv8_ws_bytes<1>();
+    if (check_kv8(kv) != LSA_OK || check_heads(hq, kv->hkv) != LSA_OK || nq <= 0 || n_idx < 0) return 0;
+    return kv8_plan(true, nq, nq, hq / kv->hkv, kv->hkv, true, ceil_div<int64_t>(n_idx, 32)).ws;
 }
 
 lsa_status lsa_kv8_sparse_attn(const lsa_kv8* kv, const uint16_t* Q, int64_t q_stride, int64_t nq, int32_t hq,
@@ -984,18 +1056,18 @@ lsa_status lsa_kv8_sparse_attn(const lsa_kv8* kv, const uint16_t* Q, int64_t q_s
     if ((s = check_kv8_attn("lsa_kv8_sparse_attn", kv, Q, q_stride, nq, hq, table, lens, n_seq, max_pages, O, ws)) != LSA_OK)
         return s;
     if (n_idx < 0) return set_error(LSA_EINVAL, "lsa_kv8_sparse_attn: n_idx < 0");
-    if (n_idx > INT32_MAX - 64) return set_error(LSA_EUNSUPPORTED, "lsa_kv8_sparse_attn: n_idx beyond 2^31");
+    if (n_idx > INT32_MAX - 128) return set_error(LSA_EUNSUPPORTED, "lsa_kv8_sparse_attn: n_idx beyond 2^31");
     if (!seq && nq != n_seq) return set_error(LSA_EINVAL, "lsa_kv8_sparse_attn: without seq, nq must equal n_seq");
     if (nq == 0) return LSA_OK;
     if (!idx && n_idx > 0) return set_error(LSA_EINVAL, "lsa_kv8_sparse_attn: idx is NULL");
-    if (ws_bytes < lsa_kv8_sparse_attn_workspace_bytes(nq, hq, kv->hkv) ||
-        (!ws && lsa_kv8_sparse_attn_workspace_bytes(nq, hq, kv->hkv) > 0))
-        return set_error(LSA_ENOSPACE, "lsa_kv8_sparse_attn: workspace too small");
     Kv8AttnArgs a = kv8_args(kv, Q, q_stride, nq, hq, table, lens, n_seq, max_pages, O, lse, ws);
     a.seq = seq; a.idx = idx; a.n_idx = n_idx;
+    const Kv8Plan p = kv8_plan(true, nq, nq, a.G, kv->hkv, true, ceil_div<int64_t>(n_idx, 32));
+    if (p.ws > 0 && (!ws || ws_bytes < p.ws)) return set_error(LSA_ENOSPACE, "lsa_kv8_sparse_attn: workspace too small");
     const cudaStream_t st = (cudaStream_t)stream;
-    if (!kv8_many_rows(nq, kv->hkv))
-        return kv->fmt == LSA_KV8_E4M3 ? launch_kv8_split<0, 1, true>(a, st) : launch_kv8_split<1, 1, true>(a, st);
+    if (!p.warps)
+        return kv->fmt == LSA_KV8_E4M3 ? launch_kv8_split<0, 1, true>(a, p, nq, true, st)
+                                       : launch_kv8_split<1, 1, true>(a, p, nq, true, st);
     {
         KTime kt_("kv8_list_kernel", st);
         const unsigned grid = (unsigned)ceil_div<int64_t>(nq * kv->hkv, kKv8ListWarps);

@@ -642,10 +642,13 @@ lsa_status lsa_kv8_write(const lsa_kv8* kv, const uint16_t* K, int64_t k_stride,
                          const int32_t* cu, const int32_t* start, const int32_t* table,
                          int32_t n_seq, int32_t max_pages, void* stream);
 
-/* Workspace bytes of lsa_kv8_attn for nq queries of n_seq sequences, and of
- * lsa_kv8_sparse_attn for nq queries (0: none needed). */
-size_t lsa_kv8_attn_workspace_bytes(int64_t nq, int32_t n_seq, int32_t hq, int32_t hkv);
-size_t lsa_kv8_sparse_attn_workspace_bytes(int64_t nq, int32_t hq, int32_t hkv);
+/* Workspace bytes of lsa_kv8_attn (one_each: cu is NULL) and of
+ * lsa_kv8_sparse_attn for the same sizes; 0 where none is needed. */
+size_t lsa_kv8_attn_workspace_bytes(const lsa_kv8* kv, int64_t nq, int32_t hq, int32_t one_each,
+                                    int32_t n_seq, int32_t max_pages, int32_t sinks,
+                                    int32_t window);
+size_t lsa_kv8_sparse_attn_workspace_bytes(const lsa_kv8* kv, int64_t nq, int32_t hq,
+                                           int32_t n_idx);
 
 /*
  * lsa_kv8_attn -- exact softmax attention of the newest tokens over their

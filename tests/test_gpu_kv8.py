@@ -172,6 +172,35 @@ def test_attention_against_64_bits(lsa, fmt, page, hkv, G, lens, new, sinks, win
     close(lse, wl, tl)
 
 
+@pytest.mark.parametrize("n_seq,hkv,G,top,spread", [(300, 1, 4, 90, 1), (700, 2, 1, 40, 1), (33, 8, 8, 500, 7), (520, 1, 2, 3000, 1)])
+def test_ragged_batches(lsa, n_seq, hkv, G, top, spread):
+    """Many sequences of very different lengths (none, one long), some without
+    a new token, in tables wider than they need."""
+    rng = np.random.default_rng(n_seq)
+    lens = (np.exp(rng.uniform(0, np.log(top), n_seq)).astype(int) * (rng.random(n_seq) < 0.9)).tolist()
+    lens[n_seq // 2] = 4 * top
+    new = rng.integers(0, spread + 1, n_seq)
+    new[-1] = spread
+    kv, table = filled(lsa, rng, [max(n, 1) for n in lens], hkv, 16, "e4m3")
+    K, V, scale = host(kv)
+    wide = np.full((n_seq, 1000), -1, np.int32)
+    wide[:, :table.shape[1]] = table
+    cu = np.concatenate([[0], np.cumsum(new)])
+    q, hq = bf16(rng.standard_normal((cu[-1], hkv * G, 128)))
+    wo, wl, to, tl = ref.attn(hq, K, V, scale, table, lens, cu, "e4m3", 2, 64)
+    for tb in (table, wide):
+        o, lse = lsa.kv8_attn(q, kv, i32(tb), i32(lens), cu=i32(cu), sinks=2, window=64)
+        close(o, wo, to)
+        close(lse, wl, tl)
+    each, heach = bf16(rng.standard_normal((n_seq, hkv * G, 128)))
+    wo, wl, to, tl = ref.attn(heach, K, V, scale, table, lens, np.arange(n_seq + 1), "e4m3")
+    for tb in (table, wide):
+        o, lse = lsa.kv8_attn(each, kv, i32(tb), i32(lens))
+        close(o, wo, to)
+        close(lse, wl, tl)
+    lsa.check_device_error()
+
+
 def random_lists(rng, nq, hkv, n_idx, lens, seq, pads=0.2):
     idx = np.full((nq, hkv, n_idx), -1, np.int32)
     for i in range(nq):
