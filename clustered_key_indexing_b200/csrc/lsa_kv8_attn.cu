@@ -211,16 +211,17 @@ __device__ __forceinline__ void kv8_pv(Kv8State<NT>& s, const uint4 (&v)[4], con
 }
 
 // Softmax of one step.  Scores in base 2, -inf where masked; vs0, vs1: the V
-// scales of keys g and g + 8 (vmax: the step's largest, warp-uniform).
-// Leaves P^T as B operands in pb.
+// scales of keys g and g + 8.  Leaves P^T as B operands in pb.
 template <int NT>
-__device__ __forceinline__ void kv8_softmax(Kv8State<NT>& s, const float (&sc)[NT][4], float vs0, float vs1, float vmax,
+__device__ __forceinline__ void kv8_softmax(Kv8State<NT>& s, const float (&sc)[NT][4], float vs0, float vs1,
                                             uint32_t (&pb)[NT][2]) {
-    bool grew = vmax > s.vref;
+    bool grew = fmaxf(vs0, vs1) > s.vref;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
         grew = grew || fmaxf(sc[nt][0], sc[nt][2]) > s.m[nt][0] + kKv8Lazy || fmaxf(sc[nt][1], sc[nt][3]) > s.m[nt][1] + kKv8Lazy;
     if (__any_sync(0xffffffffu, grew)) {
+        // the step's largest V scale: positive floats order as integers
+        const float vmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(vs0, vs1))));
         const float nref = fmaxf(vmax, s.vref), rv = s.vref / nref;
         s.vref = nref;
 #pragma unroll
@@ -303,17 +304,17 @@ struct Kv8Keys {
         }
     }
 
-    // Row of codes of an entry, -1 for none.
-    __device__ __forceinline__ int row(const Kv8AttnArgs& a, int p) const {
-        if (p < 0) return -1;
-        const int pg = p >> a.lgp;
-        if (LIST && (p >= len || pg >= a.max_pages)) {
-            raise_device_error(kErrIndexRange);
-            return -1;
-        }
-        const int pid = __ldg(table + pg);
-        if (pid < 0 || pid >= a.n_pages) {
-            raise_device_error(kErrKv8Page);
+    // Page of an entry (-1: none, or out of range).  Only the load: what it
+    // brings is looked at a chunk later.
+    __device__ __forceinline__ int page(const Kv8AttnArgs& a, int p) const {
+        const bool ok = LIST ? p >= 0 && p < len : p >= 0;
+        return ok ? __ldg(table + (p >> a.lgp)) : -1;
+    }
+
+    // Row of codes of an entry from its page, -1 for none.
+    __device__ __forceinline__ int row(const Kv8AttnArgs& a, int p, int pid) const {
+        if ((uint32_t)pid >= (uint32_t)a.n_pages) {
+            if (p >= 0) raise_device_error(LIST && p >= len ? kErrIndexRange : kErrKv8Page);
             return -1;
         }
         return (int)((((uint32_t)pid * a.hkv + g) << a.lgp) | (uint32_t)(p & ((1 << a.lgp) - 1)));
@@ -330,16 +331,14 @@ __device__ __forceinline__ Kv8Keys<true> kv8_list(const Kv8AttnArgs& a, int64_t 
     }
     r.list = ok ? a.idx + (q * a.hkv + g) * (int64_t)a.n_idx : nullptr;
     r.table = a.table + b * a.max_pages;
-    r.len = __ldg(a.lens + b);
+    r.len = min(__ldg(a.lens + b), a.max_pages << a.lgp);
     r.n_idx = a.n_idx;
     r.g = g;
     return r;
 }
 
-// The two scales of a row as bf16 halves (they are powers of two).
-__device__ __forceinline__ uint32_t kv8_scales(const Kv8AttnArgs& a, int row) {
-    const float2 s = __ldg(reinterpret_cast<const float2*>(a.scale) + (row >> a.lgp));
-    return __byte_perm(__float_as_uint(s.x), __float_as_uint(s.y), 0x7632);  // K's upper half low, V's high
+__device__ __forceinline__ float2 kv8_scales(const Kv8AttnArgs& a, int row) {
+    return __ldg(reinterpret_cast<const float2*>(a.scale) + (row >> a.lgp));
 }
 
 // Which of the 32 entries are keys, and a row for every lane.  A lane without
@@ -366,18 +365,34 @@ constexpr int kKv8Stages = 3;
 constexpr int kKv8Step = 16 * kD;                       // bytes of K (or V) in a step
 constexpr int kKv8Ring = kKv8Stages * 2 * kKv8Step;     // bytes of a warp's ring
 
-// Copies of step `st` (0, 1) of the 32 rows into ring slot `slot`.
-__device__ __forceinline__ void kv8_issue(const Kv8AttnArgs& a, uint32_t ring, int slot, int row, int st, unsigned valid) {
+// Where this lane's copies come from and go to.
+struct Kv8Copy {
+    const uint8_t* K;  // its 16-byte chunk of row 0
+    const uint8_t* V;
+    uint32_t ring, even, odd;  // places of its chunk in rows r0 and r0 + 4 of a step (r0 = lane / 8)
+};
+
+__device__ __forceinline__ Kv8Copy kv8_copy(const Kv8AttnArgs& a, uint32_t ring) {
     const int lane = threadIdx.x & 31, r0 = lane >> 3, c = lane & 7;
+    Kv8Copy p;
+    p.K = a.K + 16 * c;
+    p.V = a.V + 16 * c;
+    p.ring = ring;
+    p.even = ring + r0 * kD + ((c ^ r0) << 4);
+    p.odd = ring + (r0 + 4) * kD + ((c ^ (r0 + 4)) << 4);
+    return p;
+}
+
+// Copies of step `st` (0, 1) of the 32 rows into the ring slot at byte `slot`.
+__device__ __forceinline__ void kv8_issue(const Kv8Copy& p, int slot, int row, int st, unsigned valid) {
     if (valid) {
-        const uint32_t dst = ring + slot * 2 * kKv8Step;
+        const int r0 = (threadIdx.x & 31) >> 3;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int r = 4 * i + r0;
-            const int64_t off = (int64_t)__shfl_sync(0xffffffffu, row, 16 * st + r) * kD + 16 * c;
-            const uint32_t at = dst + r * kD + ((c ^ (r & 7)) << 4);
-            cp_async_16(at, a.K + off, 16);
-            cp_async_16(at + kKv8Step, a.V + off, 16);
+            const int64_t r = __shfl_sync(0xffffffffu, row, 16 * st + 4 * i + r0);
+            const uint32_t at = (i & 1 ? p.odd : p.even) + slot + 8 * kD * (i >> 1);
+            cp_async_16(at, p.K + r * kD, 16);
+            cp_async_16(at + kKv8Step, p.V + r * kD, 16);
         }
     }
     cp_async_commit();
@@ -449,14 +464,16 @@ __device__ __forceinline__ void kv8_pv_columns(Kv8State<NT>& s, const uint4 (&v)
 // positions of the lane's columns, -1 for no column; key: the step's first.
 template <int FMT, int NT, bool LIST>
 __device__ __forceinline__ void kv8_step(const Kv8AttnArgs& a, const Kv8Keys<LIST>& r, Kv8State<NT>& s, uint32_t slot,
-                                         uint32_t sc, int st, unsigned valid, const int (&tc)[NT][2], int key) {
+                                         float2 sc, int st, unsigned valid, const int (&tc)[NT][2], int key) {
     const int gq = (threadIdx.x & 31) >> 2;
     Kv8K k;
     kv8_read_k(slot, k);
     float x[NT][4];
     kv8_scores<FMT, NT>(s, k, x);
-    const uint32_t c0 = __shfl_sync(0xffffffffu, sc, 16 * st + gq), c1 = __shfl_sync(0xffffffffu, sc, 16 * st + gq + 8);
-    const float k0 = __uint_as_float(c0 << 16), k1 = __uint_as_float(c1 << 16);
+    // the 16 keys of a dense step lie in one page
+    const int l0 = 16 * st + (LIST ? gq : 0), l1 = 16 * st + (LIST ? gq + 8 : 0);
+    const float k0 = __shfl_sync(0xffffffffu, sc.x, l0), v0 = __shfl_sync(0xffffffffu, sc.y, l0);
+    const float k1 = LIST ? __shfl_sync(0xffffffffu, sc.x, l1) : k0, v1 = LIST ? __shfl_sync(0xffffffffu, sc.y, l1) : v0;
     // dense: every column attends all 16 keys
     const bool whole = valid == 0xFFFFu &&
                        (LIST || (key + 15 <= r.tmin && (a.W == 0 || key >= r.lo + (r.tmax - r.tmin) || key + 16 <= a.S)));
@@ -479,13 +496,8 @@ __device__ __forceinline__ void kv8_step(const Kv8AttnArgs& a, const Kv8Keys<LIS
             }
         }
     }
-    const float v0 = __uint_as_float(c0 & 0xFFFF0000u), v1 = __uint_as_float(c1 & 0xFFFF0000u);
-    // the step's largest V scale: positive floats order as integers
-    float vmax = s.vref;
-    if (__any_sync(0xffffffffu, fmaxf(v0, v1) > s.vref))
-        vmax = __uint_as_float(__reduce_max_sync(0xffffffffu, max(c0, c1) & 0xFFFF0000u));
     uint32_t pb[NT][2];
-    kv8_softmax<NT>(s, x, v0, v1, vmax, pb);
+    kv8_softmax<NT>(s, x, v0, v1, pb);
     uint4 v[4];
     kv8_read_v(slot, v);
     if constexpr (FMT == 0 && !LIST) {
@@ -505,40 +517,58 @@ __device__ __forceinline__ void kv8_step(const Kv8AttnArgs& a, const Kv8Keys<LIS
 }
 
 // Chunks [c, cend) of a row into the warp's state.  Copies run two steps ahead
-// of their use, the rows' table entries and scales a chunk further.
-template <int FMT, int NT, bool LIST>
-__device__ __forceinline__ void kv8_chunks(const Kv8AttnArgs& a, const Kv8Keys<LIST>& r, int c, int cend,
-                                           const int (&tc)[NT][2], Kv8State<NT>& s, uint32_t ring) {
-    if (c >= cend) return;
-    int row0 = r.row(a, r.entry(a, c, cend));
-    int row1 = r.row(a, r.entry(a, c + 1, cend));
-    int e2 = r.entry(a, c + 2, cend);
-    unsigned valid = kv8_fill_rows(row0);
-    kv8_issue(a, ring, 0, row0, 0, valid & 0xFFFFu);
-    kv8_issue(a, ring, 1, row0, 1, valid >> 16);
-    uint32_t sc = kv8_scales(a, row0);
-    int slot = 0;
-    for (; c < cend; ++c) {
-        const unsigned valid1 = kv8_fill_rows(row1);
-        const int key = LIST ? 0 : r.key0(c);
-        cp_async_wait<1>();
-        __syncwarp();
-        kv8_issue(a, ring, slot == 0 ? 2 : slot - 1, row1, 0, valid1 & 0xFFFFu);
-        const int e3 = r.entry(a, c + 3, cend);
-        if (valid & 0xFFFFu) kv8_step<FMT, NT, LIST>(a, r, s, ring + slot * 2 * kKv8Step, sc, 0, valid & 0xFFFFu, tc, key);
-        cp_async_wait<1>();
-        __syncwarp();
-        kv8_issue(a, ring, slot, row1, 1, valid1 >> 16);
-        const uint32_t sc1 = kv8_scales(a, row1);
-        const int row2 = r.row(a, e2);
-        slot = slot == 2 ? 0 : slot + 1;
-        if (valid >> 16) kv8_step<FMT, NT, LIST>(a, r, s, ring + slot * 2 * kKv8Step, sc, 1, valid >> 16, tc, key + 16);
-        slot = slot == 2 ? 0 : slot + 1;
-        row1 = row2; e2 = e3; sc = sc1; valid = valid1;
+// of their use, table entries and scales a chunk further, list entries two.
+// start() brings the first chunk on its way, so that Q can be read meanwhile.
+template <bool LIST>
+struct Kv8Walk {
+    Kv8Copy cp;
+    int c, cend;
+    int p1, pid1, p2;
+    unsigned valid;
+    float2 sc;
+
+    __device__ __forceinline__ void start(const Kv8AttnArgs& a, const Kv8Keys<LIST>& r, int c_, int cend_, uint32_t ring) {
+        c = c_;
+        cend = cend_;
+        cp = kv8_copy(a, ring);
+        const int p0 = r.entry(a, c, cend);
+        p1 = r.entry(a, c + 1, cend);
+        p2 = r.entry(a, c + 2, cend);
+        const int pid0 = r.page(a, p0);
+        pid1 = r.page(a, p1);
+        int row = r.row(a, p0, pid0);
+        valid = kv8_fill_rows(row);
+        kv8_issue(cp, 0, row, 0, valid & 0xFFFFu);
+        kv8_issue(cp, 2 * kKv8Step, row, 1, valid >> 16);
+        sc = kv8_scales(a, row);
     }
-    cp_async_wait<0>();
-    __syncwarp();
-}
+
+    template <int FMT, int NT>
+    __device__ __forceinline__ void run(const Kv8AttnArgs& a, const Kv8Keys<LIST>& r, const int (&tc)[NT][2], Kv8State<NT>& s) {
+        constexpr int kSlot = 2 * kKv8Step, kLast = (kKv8Stages - 1) * kSlot;
+        int slot = 0;
+        for (; c < cend; ++c) {
+            int row1 = r.row(a, p1, pid1);
+            const unsigned valid1 = kv8_fill_rows(row1);
+            const int key = LIST ? 0 : r.key0(c);
+            cp_async_wait<1>();
+            __syncwarp();
+            kv8_issue(cp, slot == 0 ? kLast : slot - kSlot, row1, 0, valid1 & 0xFFFFu);
+            const int pid2 = r.page(a, p2), p3 = r.entry(a, c + 3, cend);
+            if (valid & 0xFFFFu) kv8_step<FMT, NT, LIST>(a, r, s, cp.ring + slot, sc, 0, valid & 0xFFFFu, tc, key);
+            cp_async_wait<1>();
+            __syncwarp();
+            kv8_issue(cp, slot, row1, 1, valid1 >> 16);
+            const float2 sc1 = kv8_scales(a, row1);
+            slot = slot == kLast ? 0 : slot + kSlot;
+            if (valid >> 16) kv8_step<FMT, NT, LIST>(a, r, s, cp.ring + slot, sc, 1, valid >> 16, tc, key + 16);
+            slot = slot == kLast ? 0 : slot + kSlot;
+            p1 = p2; pid1 = pid2; p2 = p3; sc = sc1; valid = valid1;
+        }
+        cp_async_wait<0>();
+        __syncwarp();
+    }
+};
 
 // Many rows: one warp per (query, kv-head), kv-head major so that the warps
 // resident at one time read one head's rows, which keeps them in L2.
@@ -552,11 +582,13 @@ __global__ void __launch_bounds__(32 * kKv8ListWarps, 2) kv8_list_kernel(Kv8Attn
     const int hq = a.G * a.hkv;
     Kv8State<1> s;
     const uint16_t* const row[1] = {gq < a.G ? a.Q + q * a.q_stride + (int64_t)(g * a.G + gq) * kD : nullptr};
-    kv8_load_q<1>(s, row, a.scale_log2);
     const Kv8Keys<true> r = kv8_list(a, q, g);
     extern __shared__ __align__(1024) uint8_t lsm[];
     const int tc[1][2] = {{0, 0}};
-    kv8_chunks<FMT, 1, true>(a, r, 0, (a.n_idx + 31) / 32, tc, s, smem_u32(lsm) + (threadIdx.x >> 5) * kKv8Ring);
+    Kv8Walk<true> walk;
+    walk.start(a, r, 0, (a.n_idx + 31) / 32, smem_u32(lsm) + (threadIdx.x >> 5) * kKv8Ring);
+    kv8_load_q<1>(s, row, a.scale_log2);
+    walk.template run<FMT, 1>(a, r, tc, s);
     kv8_reduce_l<1>(s);
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
@@ -763,15 +795,6 @@ __global__ void __launch_bounds__(32 * kKv8Warps, NT == 1 ? 2 : 1) kv8_split_ker
 
         if (ta < tb) {
             Kv8State<NT> s;
-            const uint16_t* row[NT];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const int64_t cc = (int64_t)cg * 8 * NT + 8 * nt + gq;
-                row[nt] = cc < (int64_t)q.n * a.G
-                              ? a.Q + (q.q0 + cc / a.G) * a.q_stride + (int64_t)(g * a.G + cc % a.G) * kD : nullptr;
-            }
-            const uint16_t* const (&crow)[NT] = row;
-            kv8_load_q<NT>(s, crow, a.scale_log2);
             Kv8Keys<LIST> keys{};
             int tc[NT][2] = {};
             if constexpr (LIST) {
@@ -795,7 +818,18 @@ __global__ void __launch_bounds__(32 * kKv8Warps, NT == 1 ? 2 : 1) kv8_split_ker
                         tc[nt][c] = cc <= c1 ? first + cc / a.G : -1;
                     }
             }
-            kv8_chunks<FMT, NT, LIST>(a, keys, ta, tb, tc, s, ring);
+            Kv8Walk<LIST> walk;
+            walk.start(a, keys, ta, tb, ring);
+            const uint16_t* row[NT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const int64_t cc = (int64_t)cg * 8 * NT + 8 * nt + gq;
+                row[nt] = cc < (int64_t)q.n * a.G
+                              ? a.Q + (q.q0 + cc / a.G) * a.q_stride + (int64_t)(g * a.G + cc % a.G) * kD : nullptr;
+            }
+            const uint16_t* const (&crow)[NT] = row;
+            kv8_load_q<NT>(s, crow, a.scale_log2);
+            walk.template run<FMT, NT>(a, keys, tc, s);
             kv8_reduce_l<NT>(s);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
