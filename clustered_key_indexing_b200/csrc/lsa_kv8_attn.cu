@@ -363,13 +363,17 @@ __device__ __forceinline__ unsigned kv8_fill_rows(int& row) {
 // which makes both the copies and the operand reads free of bank conflicts.
 constexpr int kKv8Stages = 3;
 constexpr int kKv8Step = 16 * kD;                       // bytes of K (or V) in a step
-constexpr int kKv8Ring = kKv8Stages * 2 * kKv8Step;     // bytes of a warp's ring
+constexpr int kKv8Note = 32 * 8 + 32 * 4;               // a chunk's scales (float2) and rows, beside the ring
+constexpr int kKv8Ring = kKv8Stages * 2 * kKv8Step;     // bytes of a warp's ring ...
+constexpr int kKv8Warp = kKv8Ring + 2 * kKv8Note + 256; // ... and of all it has (a multiple of 1024)
+static_assert(kKv8Warp % 1024 == 0, "the ring's swizzle goes by address");
 
 // Where this lane's copies come from and go to.
 struct Kv8Copy {
     const uint8_t* K;  // its 16-byte chunk of row 0
     const uint8_t* V;
     uint32_t ring, even, odd;  // places of its chunk in rows r0 and r0 + 4 of a step (r0 = lane / 8)
+    uint32_t note;             // two chunks' scales and rows
 };
 
 __device__ __forceinline__ Kv8Copy kv8_copy(const Kv8AttnArgs& a, uint32_t ring) {
@@ -378,30 +382,48 @@ __device__ __forceinline__ Kv8Copy kv8_copy(const Kv8AttnArgs& a, uint32_t ring)
     p.K = a.K + 16 * c;
     p.V = a.V + 16 * c;
     p.ring = ring;
+    p.note = ring + kKv8Ring;
     p.even = ring + r0 * kD + ((c ^ r0) << 4);
     p.odd = ring + (r0 + 4) * kD + ((c ^ (r0 + 4)) << 4);
     return p;
-}
-
-// Copies of step `st` (0, 1) of the 32 rows into the ring slot at byte `slot`.
-__device__ __forceinline__ void kv8_issue(const Kv8Copy& p, int slot, int row, int st, unsigned valid) {
-    if (valid) {
-        const int r0 = (threadIdx.x & 31) >> 3;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t r = __shfl_sync(0xffffffffu, row, 16 * st + 4 * i + r0);
-            const uint32_t at = (i & 1 ? p.odd : p.even) + slot + 8 * kD * (i >> 1);
-            cp_async_16(at, p.K + r * kD, 16);
-            cp_async_16(at + kKv8Step, p.V + r * kD, 16);
-        }
-    }
-    cp_async_commit();
 }
 
 __device__ __forceinline__ uint4 lds_16(uint32_t p) {
     uint4 v;
     asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p));
     return v;
+}
+
+// A chunk's rows go through shared memory to the lanes that copy them: row 16
+// st + 4 i + r as word 16 st + 4 r + i, so that a lane reads its four at once.
+__device__ __forceinline__ void kv8_note_rows(uint32_t note, int row) {
+    const int e = threadIdx.x & 31;
+    asm volatile("st.shared.b32 [%0], %1;\n" ::"r"(note + 256 + 4 * ((e & 16) + 4 * (e & 3) + ((e >> 2) & 3))), "r"(row) : "memory");
+}
+
+__device__ __forceinline__ void kv8_note_scales(uint32_t note, float2 sc) {
+    asm volatile("st.shared.v2.f32 [%0], {%1, %2};\n" ::"r"(note + 8 * (threadIdx.x & 31)), "f"(sc.x), "f"(sc.y) : "memory");
+}
+
+__device__ __forceinline__ float2 kv8_scale_of(uint32_t note, int e) {
+    float2 s;
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];\n" : "=f"(s.x), "=f"(s.y) : "r"(note + 8 * e));
+    return s;
+}
+
+// Copies of step `st` (0, 1) of the noted rows into the ring slot at byte `slot`.
+__device__ __forceinline__ void kv8_issue(const Kv8Copy& p, uint32_t note, int slot, int st, unsigned valid) {
+    if (valid) {
+        const uint4 r = lds_16(note + 256 + 64 * st + 16 * ((threadIdx.x & 31) >> 3));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t row = (int32_t)word_of(r, i);
+            const uint32_t at = (i & 1 ? p.odd : p.even) + slot + 8 * kD * (i >> 1);
+            cp_async_16(at, p.K + row * kD, 16);
+            cp_async_16(at + kKv8Step, p.V + row * kD, 16);
+        }
+    }
+    cp_async_commit();
 }
 
 __device__ __forceinline__ void kv8_read_k(uint32_t slot, Kv8K& k) {
@@ -460,20 +482,19 @@ __device__ __forceinline__ void kv8_pv_columns(Kv8State<NT>& s, const uint4 (&v)
         }
 }
 
-// One step.  sc: the 32 rows' scales; valid: the step's 16 keys; tc (dense):
+// One step.  note: the 32 rows' scales; valid: the step's 16 keys; tc (dense):
 // positions of the lane's columns, -1 for no column; key: the step's first.
 template <int FMT, int NT, bool LIST>
 __device__ __forceinline__ void kv8_step(const Kv8AttnArgs& a, const Kv8Keys<LIST>& r, Kv8State<NT>& s, uint32_t slot,
-                                         float2 sc, int st, unsigned valid, const int (&tc)[NT][2], int key) {
+                                         uint32_t note, int st, unsigned valid, const int (&tc)[NT][2], int key) {
     const int gq = (threadIdx.x & 31) >> 2;
     Kv8K k;
     kv8_read_k(slot, k);
     float x[NT][4];
     kv8_scores<FMT, NT>(s, k, x);
     // the 16 keys of a dense step lie in one page
-    const int l0 = 16 * st + (LIST ? gq : 0), l1 = 16 * st + (LIST ? gq + 8 : 0);
-    const float k0 = __shfl_sync(0xffffffffu, sc.x, l0), v0 = __shfl_sync(0xffffffffu, sc.y, l0);
-    const float k1 = LIST ? __shfl_sync(0xffffffffu, sc.x, l1) : k0, v1 = LIST ? __shfl_sync(0xffffffffu, sc.y, l1) : v0;
+    const float2 s0 = kv8_scale_of(note, 16 * st + (LIST ? gq : 0)), s1 = LIST ? kv8_scale_of(note, 16 * st + gq + 8) : s0;
+    const float k0 = s0.x, v0 = s0.y, k1 = s1.x, v1 = s1.y;
     // dense: every column attends all 16 keys
     const bool whole = valid == 0xFFFFu &&
                        (LIST || (key + 15 <= r.tmin && (a.W == 0 || key >= r.lo + (r.tmax - r.tmin) || key + 16 <= a.S)));
@@ -525,7 +546,6 @@ struct Kv8Walk {
     int c, cend;
     int p1, pid1, p2;
     unsigned valid;
-    float2 sc;
 
     __device__ __forceinline__ void start(const Kv8AttnArgs& a, const Kv8Keys<LIST>& r, int c_, int cend_, uint32_t ring) {
         c = c_;
@@ -538,32 +558,40 @@ struct Kv8Walk {
         pid1 = r.page(a, p1);
         int row = r.row(a, p0, pid0);
         valid = kv8_fill_rows(row);
-        kv8_issue(cp, 0, row, 0, valid & 0xFFFFu);
-        kv8_issue(cp, 2 * kKv8Step, row, 1, valid >> 16);
-        sc = kv8_scales(a, row);
+        kv8_note_rows(cp.note, row);
+        __syncwarp();
+        kv8_issue(cp, cp.note, 0, 0, valid & 0xFFFFu);
+        kv8_issue(cp, cp.note, 2 * kKv8Step, 1, valid >> 16);
+        kv8_note_scales(cp.note, kv8_scales(a, row));
     }
 
     template <int FMT, int NT>
     __device__ __forceinline__ void run(const Kv8AttnArgs& a, const Kv8Keys<LIST>& r, const int (&tc)[NT][2], Kv8State<NT>& s) {
         constexpr int kSlot = 2 * kKv8Step, kLast = (kKv8Stages - 1) * kSlot;
         int slot = 0;
+        uint32_t note = cp.note, note1 = cp.note + kKv8Note;
         for (; c < cend; ++c) {
             int row1 = r.row(a, p1, pid1);
             const unsigned valid1 = kv8_fill_rows(row1);
             const int key = LIST ? 0 : r.key0(c);
-            cp_async_wait<1>();
-            __syncwarp();
-            kv8_issue(cp, slot == 0 ? kLast : slot - kSlot, row1, 0, valid1 & 0xFFFFu);
-            const int pid2 = r.page(a, p2), p3 = r.entry(a, c + 3, cend);
-            if (valid & 0xFFFFu) kv8_step<FMT, NT, LIST>(a, r, s, cp.ring + slot, sc, 0, valid & 0xFFFFu, tc, key);
-            cp_async_wait<1>();
-            __syncwarp();
-            kv8_issue(cp, slot, row1, 1, valid1 >> 16);
+            kv8_note_rows(note1, row1);
             const float2 sc1 = kv8_scales(a, row1);
+            cp_async_wait<1>();
+            __syncwarp();
+            kv8_issue(cp, note1, slot == 0 ? kLast : slot - kSlot, 0, valid1 & 0xFFFFu);
+            const int pid2 = r.page(a, p2), p3 = r.entry(a, c + 3, cend);
+            if (valid & 0xFFFFu) kv8_step<FMT, NT, LIST>(a, r, s, cp.ring + slot, note, 0, valid & 0xFFFFu, tc, key);
+            cp_async_wait<1>();
+            __syncwarp();
+            kv8_issue(cp, note1, slot, 1, valid1 >> 16);
             slot = slot == kLast ? 0 : slot + kSlot;
-            if (valid >> 16) kv8_step<FMT, NT, LIST>(a, r, s, cp.ring + slot, sc, 1, valid >> 16, tc, key + 16);
+            if (valid >> 16) kv8_step<FMT, NT, LIST>(a, r, s, cp.ring + slot, note, 1, valid >> 16, tc, key + 16);
             slot = slot == kLast ? 0 : slot + kSlot;
-            p1 = p2; pid1 = pid2; p2 = p3; sc = sc1; valid = valid1;
+            kv8_note_scales(note1, sc1);
+            const uint32_t other = note;
+            note = note1;
+            note1 = other;
+            p1 = p2; pid1 = pid2; p2 = p3; valid = valid1;
         }
         cp_async_wait<0>();
         __syncwarp();
@@ -586,7 +614,7 @@ __global__ void __launch_bounds__(32 * kKv8ListWarps, 2) kv8_list_kernel(Kv8Attn
     extern __shared__ __align__(1024) uint8_t lsm[];
     const int tc[1][2] = {{0, 0}};
     Kv8Walk<true> walk;
-    walk.start(a, r, 0, (a.n_idx + 31) / 32, smem_u32(lsm) + (threadIdx.x >> 5) * kKv8Ring);
+    walk.start(a, r, 0, (a.n_idx + 31) / 32, smem_u32(lsm) + (threadIdx.x >> 5) * kKv8Warp);
     kv8_load_q<1>(s, row, a.scale_log2);
     walk.template run<FMT, 1>(a, r, tc, s);
     kv8_reduce_l<1>(s);
@@ -758,9 +786,9 @@ template <int FMT, int NT, bool LIST>
 __global__ void __launch_bounds__(32 * kKv8Warps, NT == 1 ? 2 : 1) kv8_split_kernel(Kv8AttnArgs a, int least) {
     extern __shared__ __align__(1024) uint8_t ksm[];
     __shared__ float sml[kKv8Warps * 8 * NT * 2];                 // (m, l) of every warp's columns
-    const uint32_t ring = smem_u32(ksm) + (threadIdx.x >> 5) * kKv8Ring;
+    const uint32_t ring = smem_u32(ksm) + (threadIdx.x >> 5) * kKv8Warp;
     // a warp's sums go where its ring was: [8 NT][kKv8Pad] floats
-    auto so = [&](int w) { return reinterpret_cast<float*>(ksm + w * kKv8Ring); };
+    auto so = [&](int w) { return reinterpret_cast<float*>(ksm + w * kKv8Warp); };
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, gq = lane >> 2, tq = lane & 3;
     Kv8Seq q;
     int64_t b, w0, w1;
@@ -981,7 +1009,7 @@ template <int FMT, int NT, bool LIST>
 static lsa_status launch_kv8_split(Kv8AttnArgs a, const Kv8Plan& p, int64_t n_seq, bool one_each, cudaStream_t st) {
     const int n = p.rows_per_seq > 0 ? (int)(p.rows_per_seq * n_seq) : kv8_ctas<NT>();
     a.rows_per_seq = (int32_t)p.rows_per_seq;
-    const size_t smem = (size_t)kKv8Warps * kKv8Ring;
+    const size_t smem = (size_t)kKv8Warps * kKv8Warp;
     cudaFuncSetAttribute(kv8_split_kernel<FMT, NT, LIST>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     lsa_status s;
     {
@@ -1106,7 +1134,7 @@ lsa_status lsa_kv8_sparse_attn(const lsa_kv8* kv, const uint16_t* Q, int64_t q_s
         KTime kt_("kv8_list_kernel", st);
         const unsigned grid = (unsigned)ceil_div<int64_t>(nq * kv->hkv, kKv8ListWarps);
         auto kern = kv->fmt == LSA_KV8_E4M3 ? kv8_list_kernel<0> : kv8_list_kernel<1>;
-        const int smem = kKv8ListWarps * kKv8Ring;
+        const int smem = kKv8ListWarps * kKv8Warp;
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         kern<<<grid, 32 * kKv8ListWarps, smem, st>>>(a);
     }
