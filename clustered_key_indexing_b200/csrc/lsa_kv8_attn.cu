@@ -8,13 +8,13 @@
 //   O^T += V^T P^T.
 // Rows of codes travel through a per-warp ring in shared memory (cp.async, two
 // steps ahead; through registers instead, with one step ahead, a million
-// tokens took 667 us against 420: too few bytes in flight) and are read 16
-// bytes a lane in an order that makes them MMA operands without a shuffle: the
-// K dimension of S^T is a permutation of the 128 dims (lane (g, t) holds dims
-// 32 t .. + 31 of key rows g and g + 8, Q follows the same order), and the M
-// dimension of O^T is one too (lane (g, t) holds dims 16 g .. + 15 of key rows
-// 2t, 2t+1, 2t+8, 2t+9; byte pairs of two rows are interleaved
-// with one byte permute).  Codes become fp16 exactly; Q is divided by its
+// tokens took 667 us against 420: too few bytes in flight) and are read in an
+// order that makes them MMA operands without a shuffle: the K dimension of S^T
+// is a permutation of the 128 dims (lane (g, t) holds dims 32 t .. + 31 of two
+// key rows, 16 bytes a load; Q follows the same order), its M dimension one of
+// the 16 keys, which is the order in which the transposing 8-bit ldmatrix
+// leaves V's keys (byte permutes of row-wise loads in its place cost an eighth
+// of the step's integer instructions).  Codes become fp16 exactly; Q is divided by its
 // row's power of two and becomes fp16 (exact to 2^-17 of the row's largest
 // element, absolute error 2^-25 of it below that; an e4m3 mma.sync converts
 // both operands to fp16 itself and was slower); P is fp16 with 12 bits of
@@ -185,33 +185,31 @@ __device__ __forceinline__ void kv8_scores(const Kv8State<NT>& s, const Kv8K& k,
         for (int i = 0; i < 4; ++i) sc[nt][i] = c[nt][0][i] + c[nt][1][i];
 }
 
-// The interleaved fp16 A operands of V^T for words j of the lane's four rows:
-// m-tiles 2j (dims 16 g + 4 j, + 1) and 2j + 1 (dims + 2, + 3).
-template <int FMT>
-__device__ __forceinline__ void kv8_v_operands(const uint32_t (&w)[4], uint32_t (&a0)[4], uint32_t (&a1)[4]) {
-    kv8_f16<FMT>(__byte_perm(w[0], w[1], 0x5140), a0[0], a0[1]);
-    kv8_f16<FMT>(__byte_perm(w[2], w[3], 0x5140), a0[2], a0[3]);
-    kv8_f16<FMT>(__byte_perm(w[0], w[1], 0x7362), a1[0], a1[1]);
-    kv8_f16<FMT>(__byte_perm(w[2], w[3], 0x7362), a1[2], a1[3]);
-}
+// V^T of a step as ldmatrix transposes it: register 2 i (+ 1) of the pair i / 2
+// holds dim 8 i + g (of 16 i..: see kv8_read_v) of keys 4 t .. 4 t + 3.
+struct Kv8V {
+    uint32_t w[16];  // w[2 mt], w[2 mt + 1]: dims 16 mt + g and 16 mt + g + 8
+};
 
+// O^T += V^T P^T: keys 4 t, 4 t + 1 are the MMA's k = 2 t, 2 t + 1 and keys
+// 4 t + 2, + 3 its k = 2 t + 8, + 9, which is the order of S^T's rows (kv8_key).
 template <int FMT, int NT>
-__device__ __forceinline__ void kv8_pv(Kv8State<NT>& s, const uint4 (&v)[4], const uint32_t (&pb)[NT][2]) {
+__device__ __forceinline__ void kv8_pv(Kv8State<NT>& s, const Kv8V& v, const uint32_t (&pb)[NT][2]) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const uint32_t w[4] = {word_of(v[0], j), word_of(v[1], j), word_of(v[2], j), word_of(v[3], j)};
-        uint32_t a0[4], a1[4];
-        kv8_v_operands<FMT>(w, a0, a1);
+    for (int mt = 0; mt < 8; ++mt) {
+        uint32_t a[4];
+        kv8_f16<FMT>(v.w[2 * mt], a[0], a[2]);
+        kv8_f16<FMT>(v.w[2 * mt + 1], a[1], a[3]);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            mma_16816_f16(s.o[nt][2 * j], a0, pb[nt][0], pb[nt][1]);
-            mma_16816_f16(s.o[nt][2 * j + 1], a1, pb[nt][0], pb[nt][1]);
-        }
+        for (int nt = 0; nt < NT; ++nt) mma_16816_f16(s.o[nt][mt], a, pb[nt][0], pb[nt][1]);
     }
 }
 
+// Key of a step that row g of S^T stands for; row g + 8 is the key two after.
+__device__ __forceinline__ int kv8_key(int gq) { return 4 * (gq >> 1) + (gq & 1); }
+
 // Softmax of one step.  Scores in base 2, -inf where masked; vs0, vs1: the V
-// scales of keys g and g + 8.  Leaves P^T as B operands in pb.
+// scales of rows g and g + 8.  Leaves P^T as B operands in pb.
 template <int NT>
 __device__ __forceinline__ void kv8_softmax(Kv8State<NT>& s, const float (&sc)[NT][4], float vs0, float vs1,
                                             uint32_t (&pb)[NT][2]) {
@@ -427,28 +425,30 @@ __device__ __forceinline__ void kv8_issue(const Kv8Copy& p, uint32_t note, int s
 }
 
 __device__ __forceinline__ void kv8_read_k(uint32_t slot, Kv8K& k) {
-    const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
-    const uint32_t p = slot + gq * kD + (((2 * tq) ^ gq) << 4);
+    const int lane = threadIdx.x & 31, tq = lane & 3, key = kv8_key(lane >> 2);
+    const uint32_t p = slot + key * kD + (((2 * tq) ^ (key & 7)) << 4), q = (p ^ 32u) + 2 * kD;
     k.a[0] = lds_16(p);
     k.a[1] = lds_16(p ^ 16u);
-    k.b[0] = lds_16(p + 8 * kD);
-    k.b[1] = lds_16((p ^ 16u) + 8 * kD);
+    k.b[0] = lds_16(q);
+    k.b[1] = lds_16(q ^ 16u);
 }
 
-__device__ __forceinline__ void kv8_read_v(uint32_t slot, uint4 (&v)[4]) {
-    const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
-    const uint32_t p = slot + kKv8Step + 2 * tq * kD + ((gq ^ (2 * tq)) << 4);
-    v[0] = lds_16(p);
-    v[1] = lds_16((p ^ 16u) + kD);
-    v[2] = lds_16(p + 8 * kD);
-    v[3] = lds_16((p ^ 16u) + 9 * kD);
+__device__ __forceinline__ void kv8_read_v(uint32_t slot, Kv8V& v) {
+    const int lane = threadIdx.x & 31;
+    // lanes 0 .. 15 address the rows of dims 32 i .. + 15, the others of + 16 .. + 31
+    const uint32_t p = slot + kKv8Step + (lane & 15) * kD + (((lane >> 4) ^ (lane & 7)) << 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];\n"
+                     : "=r"(v.w[4 * i]), "=r"(v.w[4 * i + 1]), "=r"(v.w[4 * i + 2]), "=r"(v.w[4 * i + 3])
+                     : "r"(p ^ (32u * i)));
 }
 
 // O^T += V^T P^T for a step whose mask differs between columns and which holds
 // a NaN value: column by column, so that a NaN under one column's mask does
 // not reach it through 0 * NaN.
 template <int FMT, int NT>
-__device__ __forceinline__ void kv8_pv_columns(Kv8State<NT>& s, const uint4 (&v)[4], const uint32_t (&pb)[NT][2],
+__device__ __forceinline__ void kv8_pv_columns(Kv8State<NT>& s, const Kv8V& v, const uint32_t (&pb)[NT][2],
                                                const int (&tc)[NT][2], int key, int W, int S) {
     const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
 #pragma unroll
@@ -457,26 +457,23 @@ __device__ __forceinline__ void kv8_pv_columns(Kv8State<NT>& s, const uint4 (&v)
         for (int c = 0; c < 8; ++c) {
             const int t = __shfl_sync(0xffffffffu, (c & 1) ? tc[nt][1] : tc[nt][0], c >> 1);
             const uint32_t b0 = gq == c ? pb[nt][0] : 0u, b1 = gq == c ? pb[nt][1] : 0u;
-            bool keep[4];
+            uint32_t keep = 0u;  // bytes of keys 4 t .. 4 t + 3 that the column attends
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int j = key + 2 * tq + (i & 1) + 8 * (i >> 1);
-                keep[i] = j <= t && (W == 0 || j > t - W || j < S);
+                const int j = key + 4 * tq + i;
+                if (j <= t && (W == 0 || j > t - W || j < S)) keep |= 0xFFu << (8 * i);
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t w[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = keep[i] ? word_of(v[i], j) : 0u;
-                uint32_t a0[4], a1[4];
-                kv8_v_operands<FMT>(w, a0, a1);
-                float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
-                mma_16816_f16(x, a0, b0, b1);
-                mma_16816_f16(y, a1, b0, b1);
+            for (int mt = 0; mt < 8; ++mt) {
+                uint32_t a[4];
+                kv8_f16<FMT>(v.w[2 * mt] & keep, a[0], a[2]);
+                kv8_f16<FMT>(v.w[2 * mt + 1] & keep, a[1], a[3]);
+                float x[4] = {0.f, 0.f, 0.f, 0.f};
+                mma_16816_f16(x, a, b0, b1);
                 if (tq == (c >> 1)) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if ((i & 1) == (c & 1)) { s.o[nt][2 * j][i] += x[i]; s.o[nt][2 * j + 1][i] += y[i]; }
+                        if ((i & 1) == (c & 1)) s.o[nt][mt][i] += x[i];
                 }
             }
         }
@@ -487,13 +484,13 @@ __device__ __forceinline__ void kv8_pv_columns(Kv8State<NT>& s, const uint4 (&v)
 template <int FMT, int NT, bool LIST>
 __device__ __forceinline__ void kv8_step(const Kv8AttnArgs& a, const Kv8Keys<LIST>& r, Kv8State<NT>& s, uint32_t slot,
                                          uint32_t note, int st, unsigned valid, const int (&tc)[NT][2], int key) {
-    const int gq = (threadIdx.x & 31) >> 2;
+    const int kr = kv8_key((threadIdx.x & 31) >> 2);  // this lane's keys of the step: kr and kr + 2
     Kv8K k;
     kv8_read_k(slot, k);
     float x[NT][4];
     kv8_scores<FMT, NT>(s, k, x);
     // the 16 keys of a dense step lie in one page
-    const float2 s0 = kv8_scale_of(note, 16 * st + (LIST ? gq : 0)), s1 = LIST ? kv8_scale_of(note, 16 * st + gq + 8) : s0;
+    const float2 s0 = kv8_scale_of(note, 16 * st + (LIST ? kr : 0)), s1 = LIST ? kv8_scale_of(note, 16 * st + kr + 2) : s0;
     const float k0 = s0.x, v0 = s0.y, k1 = s1.x, v1 = s1.y;
     // dense: every column attends all 16 keys
     const bool whole = valid == 0xFFFFu &&
@@ -507,7 +504,7 @@ __device__ __forceinline__ void kv8_step(const Kv8AttnArgs& a, const Kv8Keys<LIS
         if (!whole) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int j = gq + 8 * (i >> 1);
+                const int j = kr + 2 * (i >> 1);
                 bool ok = (valid >> j) & 1u;
                 if constexpr (!LIST) {
                     const int t = tc[nt][i & 1];
@@ -519,15 +516,13 @@ __device__ __forceinline__ void kv8_step(const Kv8AttnArgs& a, const Kv8Keys<LIS
     }
     uint32_t pb[NT][2];
     kv8_softmax<NT>(s, x, v0, v1, pb);
-    uint4 v[4];
+    Kv8V v;
     kv8_read_v(slot, v);
     if constexpr (FMT == 0 && !LIST) {
         if (!whole && r.tmin != r.tmax) {
             bool nan = false;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) nan = nan || __vcmpeq4(word_of(v[i], j) & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0u;
+            for (int i = 0; i < 16; ++i) nan = nan || __vcmpeq4(v.w[i] & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0u;
             if (__any_sync(0xffffffffu, nan)) {
                 kv8_pv_columns<FMT, NT>(s, v, pb, tc, key, a.W, a.S);
                 return;
@@ -618,19 +613,22 @@ __global__ void __launch_bounds__(32 * kKv8ListWarps, 2) kv8_list_kernel(Kv8Attn
     kv8_load_q<1>(s, row, a.scale_log2);
     walk.template run<FMT, 1>(a, r, tc, s);
     kv8_reduce_l<1>(s);
+    // through shared memory (the ring's), [8][128] bf16, to whole lines
+    uint16_t* os = reinterpret_cast<uint16_t*>(lsm + (threadIdx.x >> 5) * kKv8Warp);
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-        if (2 * tq + c >= a.G) continue;
         const float l = s.l[0][c], f = l > 0.f || l != l ? s.vref / l : 0.f;
-        const int64_t orow = q * hq + g * a.G + 2 * tq + c;
-        uint32_t w[8];
 #pragma unroll
-        for (int mt = 0; mt < 8; ++mt) w[mt] = pack_bf16x2(s.o[0][mt][c] * f, s.o[0][mt][2 + c] * f);
-        uint4* op = reinterpret_cast<uint4*>(a.O + orow * kD + 16 * gq);
-        op[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        op[1] = make_uint4(w[4], w[5], w[6], w[7]);
-        if (a.lse && gq == 0) a.lse[orow] = l > 0.f || l != l ? s.m[0][c] - kKv8Head + log2f(l) : -CUDART_INF_F;
+        for (int mt = 0; mt < 8; ++mt) {
+            os[(2 * tq + c) * kD + 16 * mt + gq] = bf16_bits(s.o[0][mt][c] * f);
+            os[(2 * tq + c) * kD + 16 * mt + gq + 8] = bf16_bits(s.o[0][mt][2 + c] * f);
+        }
+        if (a.lse && gq == 0 && 2 * tq + c < a.G)
+            a.lse[q * hq + g * a.G + 2 * tq + c] = l > 0.f || l != l ? s.m[0][c] - kKv8Head + log2f(l) : -CUDART_INF_F;
     }
+    __syncwarp();
+    uint4* orow = reinterpret_cast<uint4*>(a.O + (q * hq + g * a.G) * kD);
+    for (int c = lane; c < a.G * kD / 8; c += 32) orow[c] = reinterpret_cast<const uint4*>(os)[c];
 }
 
 // ------------------------------------------------ rows split over the GPU
@@ -864,11 +862,12 @@ __global__ void __launch_bounds__(32 * kKv8Warps, NT == 1 ? 2 : 1) kv8_split_ker
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     const int col = wid * 8 * NT + 8 * nt + 2 * tq + c;
-                    float4* p = reinterpret_cast<float4*>(so(wid) + (8 * nt + 2 * tq + c) * kKv8Pad + 16 * gq);
+                    float* p = so(wid) + (8 * nt + 2 * tq + c) * kKv8Pad + gq;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        p[j] = make_float4(s.o[nt][2 * j][c] * s.vref, s.o[nt][2 * j][2 + c] * s.vref,
-                                           s.o[nt][2 * j + 1][c] * s.vref, s.o[nt][2 * j + 1][2 + c] * s.vref);
+                    for (int mt = 0; mt < 8; ++mt) {
+                        p[16 * mt] = s.o[nt][mt][c] * s.vref;
+                        p[16 * mt + 8] = s.o[nt][mt][2 + c] * s.vref;
+                    }
                     if (gq == 0) { sml[2 * col] = s.m[nt][c]; sml[2 * col + 1] = s.l[nt][c]; }
                 }
         } else {
