@@ -93,32 +93,35 @@ __device__ __forceinline__ void kv8_new_tokens(const Kv8WriteArgs& a, int b, int
     }
 }
 
-// One CTA per (page the call touches, kv-head, K or V): the page's new rows
-// are held in registers (16 rows a pass, 16 lanes of 16 bytes a row) between
+// One CTA per (page the call touches, kv-head), for K and V both where their
+// rows fit the registers (pages of up to 64 tokens; else blockIdx.y tells which):
+// the new rows are held (16 rows a pass, 16 lanes of 16 bytes a row) between
 // the pass that finds their largest magnitude and the one that writes their
-// codes, so HBM sees each input once and each code once.  blockIdx.x counts
-// the touched pages of all sequences; every CTA finds its own by a scan over
-// the sequences' page counts.
+// codes, so HBM sees each input once and each code once.  The heads of a page
+// are neighbours in the grid: together they read whole token rows.  Every CTA
+// finds its page by a scan over the sequences' page counts.
 template <int FMT, int PASSES>
 __global__ void __launch_bounds__(256) kv8_write_kernel(Kv8WriteArgs a) {
-    constexpr int page = 16 * PASSES;
+    constexpr int page = 16 * PASSES, NKV = PASSES <= 4 ? 2 : 1;
     __shared__ int64_t s_at[4];       // first new row's position, one past the last, first row of the call, page index
     __shared__ int32_t s_seq;
-    __shared__ uint32_t s_max[8];
+    __shared__ uint32_t s_max[NKV][8];
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    const int64_t item = blockIdx.x / a.hkv;
+    const int h = blockIdx.x % a.hkv;
     if (wid == 0) {
         if (a.cu == nullptr) {  // one token per sequence: touched page number b is sequence b's
             if (lane == 0) {
                 int64_t q0, n, s0;
-                kv8_new_tokens(a, (int)blockIdx.x, page, q0, n, s0);
-                s_seq = n > 0 ? (int32_t)blockIdx.x : -1;
+                kv8_new_tokens(a, (int)item, page, q0, n, s0);
+                s_seq = n > 0 ? (int32_t)item : -1;
                 s_at[0] = s0; s_at[1] = s0 + n; s_at[2] = q0; s_at[3] = s0 / page;
             }
         } else {
             if (lane == 0) s_seq = -1;
             __syncwarp();
             int64_t base = 0;
-            for (int b0 = 0; b0 < a.n_seq && base <= (int64_t)blockIdx.x; b0 += 32) {
+            for (int b0 = 0; b0 < a.n_seq && base <= item; b0 += 32) {
                 const int b = b0 + lane;
                 int64_t q0 = 0, n = 0, s0 = 0, m = 0;
                 if (b < a.n_seq) kv8_new_tokens(a, b, page, q0, n, s0);
@@ -129,7 +132,7 @@ __global__ void __launch_bounds__(256) kv8_write_kernel(Kv8WriteArgs a) {
                     const int64_t up = __shfl_up_sync(0xffffffffu, inc, off);
                     if (lane >= off) inc += up;
                 }
-                const int64_t k = (int64_t)blockIdx.x - (base + inc - m);
+                const int64_t k = item - (base + inc - m);
                 if (k >= 0 && k < m) {
                     s_seq = b;
                     s_at[0] = s0; s_at[1] = s0 + n; s_at[2] = q0; s_at[3] = s0 / page + k;
@@ -141,74 +144,86 @@ __global__ void __launch_bounds__(256) kv8_write_kernel(Kv8WriteArgs a) {
     __syncthreads();
     const int seq = s_seq;
     if (seq < 0) return;
-    const int h = blockIdx.y, kv = blockIdx.z;
     const int64_t p0 = s_at[0], p1 = s_at[1], pg = s_at[3];
+    const int r0 = (int)max((int64_t)0, p0 - pg * page);                   // rows below r0 were written before
+    const int r1 = (int)min((int64_t)page, p1 - pg * page);
+    const int rr = tid >> 4, c = tid & 15;
+
+    uint4 x[NKV][PASSES];
+#pragma unroll
+    for (int j = 0; j < NKV; ++j) {
+        const bool v = NKV == 2 ? j == 1 : blockIdx.y == 1;
+        const int64_t stride = v ? a.v_stride : a.k_stride;
+        const uint16_t* src = (v ? a.V : a.K) + (s_at[2] + pg * page - p0) * stride + (int64_t)h * kD;  // row 0 of the page
+#pragma unroll
+        for (int i = 0; i < PASSES; ++i) {
+            const int r = 16 * i + rr;
+            x[j][i] = make_uint4(0u, 0u, 0u, 0u);
+            if (r >= r0 && r < r1) x[j][i] = __ldcs(reinterpret_cast<const uint4*>(src + r * stride + c * 8));
+        }
+    }
     const int64_t pid = a.table[(int64_t)seq * a.max_pages + pg];
     if (pid < 0 || pid >= a.n_pages) {
         if (tid == 0) raise_device_error(kErrKv8Page);
         return;
     }
-    const int r0 = (int)max((int64_t)0, p0 - pg * page);                   // rows below r0 were written before
-    const int r1 = (int)min((int64_t)page, p1 - pg * page);
-    const int64_t stride = kv ? a.v_stride : a.k_stride;
-    const uint16_t* src = (kv ? a.V : a.K) + (s_at[2] + pg * page - p0) * stride + (int64_t)h * kD;  // row 0 of the page
-    uint8_t* dst = (kv ? a.Vp : a.Kp) + (pid * a.hkv + h) * (int64_t)page * kD;
-    float* sp = a.scale + (pid * a.hkv + h) * 2 + kv;
-    const int rr = tid >> 4, c = tid & 15;
-
-    uint4 x[PASSES];
-    uint32_t mx = 0u;
+    float* sp = a.scale + (pid * a.hkv + h) * 2;
+    float old[NKV];
 #pragma unroll
-    for (int i = 0; i < PASSES; ++i) {
-        const int r = 16 * i + rr;
-        x[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (r >= r0 && r < r1) x[i] = *reinterpret_cast<const uint4*>(src + r * stride + c * 8);
-    }
+    for (int j = 0; j < NKV; ++j) {
+        old[j] = r0 > 0 ? sp[NKV == 2 ? j : blockIdx.y] : 0.f;
+        uint32_t mx = 0u;
 #pragma unroll
-    for (int i = 0; i < PASSES; ++i) {
-        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        for (int i = 0; i < PASSES; ++i) {
+            const uint32_t w[4] = {x[j][i].x, x[j][i].y, x[j][i].z, x[j][i].w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t lo = w[j] & 0x7FFFu, hi = (w[j] >> 16) & 0x7FFFu;  // finite magnitudes order as integers
-            mx = max(mx, lo < 0x7F80u ? lo : 0u);
-            mx = max(mx, hi < 0x7F80u ? hi : 0u);
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t lo = w[e] & 0x7FFFu, hi = (w[e] >> 16) & 0x7FFFu;  // finite magnitudes order as integers
+                mx = max(mx, lo < 0x7F80u ? lo : 0u);
+                mx = max(mx, hi < 0x7F80u ? hi : 0u);
+            }
         }
+        mx = __reduce_max_sync(0xffffffffu, mx);
+        if (lane == 0) s_max[j][wid] = mx;
     }
-    mx = __reduce_max_sync(0xffffffffu, mx);
-    if (lane == 0) s_max[wid] = mx;
-    const float old = r0 > 0 ? *sp : 0.f;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) mx = max(mx, s_max[i]);
-    const int e = kv8_exp<FMT>(mx);
-    const float need = pow2f(e);
-    if (r0 > 0 && need > old) {
-        // the open page's scale grows: its kept rows move to the new one
-        const float f = old * pow2f(-e);
-        for (int i = tid; i < r0 * (kD / 4); i += 256) {
-            uint32_t* p = reinterpret_cast<uint32_t*>(dst) + i;
-            float v[4];
-            kv8_unpack4<FMT>(*p, v);
-            *p = kv8_pack4<FMT>(v[0] * f, v[1] * f, v[2] * f, v[3] * f);
-        }
-    }
-    const float s = r0 > 0 ? fmaxf(need, old) : need;
-    const float inv = r0 > 0 && old >= need ? 1.0f / old : pow2f(-e);  // a power of two: exact
+    for (int j = 0; j < NKV; ++j) {
+        const bool v = NKV == 2 ? j == 1 : blockIdx.y == 1;
+        uint8_t* dst = (v ? a.Vp : a.Kp) + (pid * a.hkv + h) * (int64_t)page * kD;
+        uint32_t mx = 0u;
 #pragma unroll
-    for (int i = 0; i < PASSES; ++i) {
-        const int r = 16 * i + rr;
-        if (r < r0 || r >= r1) continue;
-        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-        float v[8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[2 * j] = __uint_as_float(w[j] << 16) * inv;
-            v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u) * inv;
+        for (int i = 0; i < 8; ++i) mx = max(mx, s_max[j][i]);
+        const int e = kv8_exp<FMT>(mx);
+        const float need = pow2f(e);
+        if (r0 > 0 && need > old[j]) {
+            // the open page's scale grows: its kept rows move to the new one
+            const float f = old[j] * pow2f(-e);
+            for (int i = tid; i < r0 * (kD / 4); i += 256) {
+                uint32_t* p = reinterpret_cast<uint32_t*>(dst) + i;
+                float y[4];
+                kv8_unpack4<FMT>(*p, y);
+                *p = kv8_pack4<FMT>(y[0] * f, y[1] * f, y[2] * f, y[3] * f);
+            }
         }
-        *reinterpret_cast<uint2*>(dst + r * kD + c * 8) =
-            make_uint2(kv8_pack4<FMT>(v[0], v[1], v[2], v[3]), kv8_pack4<FMT>(v[4], v[5], v[6], v[7]));
+        const float s = r0 > 0 ? fmaxf(need, old[j]) : need;
+        const float inv = r0 > 0 && old[j] >= need ? 1.0f / old[j] : pow2f(-e);  // a power of two: exact
+#pragma unroll
+        for (int i = 0; i < PASSES; ++i) {
+            const int r = 16 * i + rr;
+            if (r < r0 || r >= r1) continue;
+            const uint32_t w[4] = {x[j][i].x, x[j][i].y, x[j][i].z, x[j][i].w};
+            float y[8];
+#pragma unroll
+            for (int e2 = 0; e2 < 4; ++e2) {
+                y[2 * e2] = __uint_as_float(w[e2] << 16) * inv;
+                y[2 * e2 + 1] = __uint_as_float(w[e2] & 0xFFFF0000u) * inv;
+            }
+            *reinterpret_cast<uint2*>(dst + r * kD + c * 8) =
+                make_uint2(kv8_pack4<FMT>(y[0], y[1], y[2], y[3]), kv8_pack4<FMT>(y[4], y[5], y[6], y[7]));
+        }
+        if (tid == 0) sp[v] = s;
     }
-    if (tid == 0) *sp = s;
 }
 
 // Page copies.  The pairs travel in the launch's own arguments: no upload, and
@@ -296,7 +311,7 @@ lsa_status lsa_kv8_write(const lsa_kv8* kv, const uint16_t* K, int64_t k_stride,
     if (!aligned16(K) || !aligned16(V)) return set_error(LSA_EINVAL, "lsa_kv8_write: K and V must be 16-byte aligned");
     // pages a sequence touches: at most n / page + 2
     const int64_t items = cu ? n_tokens / kv->page + 2 * (int64_t)n_seq : n_seq;
-    if (n_tokens > INT32_MAX || items > INT32_MAX) return set_error(LSA_EUNSUPPORTED, "lsa_kv8_write: n_tokens beyond 2^31");
+    if (n_tokens > INT32_MAX || items * kv->hkv > INT32_MAX) return set_error(LSA_EUNSUPPORTED, "lsa_kv8_write: n_tokens beyond 2^31");
     Kv8WriteArgs a{};
     a.K = K; a.V = V; a.k_stride = k_stride; a.v_stride = v_stride;
     a.Kp = kv->K; a.Vp = kv->V; a.scale = kv->scale;
@@ -305,7 +320,7 @@ lsa_status lsa_kv8_write(const lsa_kv8* kv, const uint16_t* K, int64_t k_stride,
     const cudaStream_t st = (cudaStream_t)stream;
     {
         KTime kt_("kv8_write_kernel", st);
-        const dim3 grid((unsigned)items, (unsigned)kv->hkv, 2);
+        const dim3 grid((unsigned)(items * kv->hkv), kv->page <= 64 ? 1 : 2);
         if (kv->fmt == LSA_KV8_E4M3) launch_kv8_write<0>(a, kv->page, grid, st);
         else launch_kv8_write<1>(a, kv->page, grid, st);
     }
