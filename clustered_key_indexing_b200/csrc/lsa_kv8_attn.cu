@@ -907,9 +907,33 @@ __global__ void __launch_bounds__(32 * kKv8Warps, NT == 1 ? 2 : 1) kv8_split_ker
     }
 }
 
-// Joins one column (blockIdx.y) of the row that crosses the end of CTA c's
-// range, if that row began inside it: every warp takes each eighth state, a
-// lane four of its sums.
+// One column of n partial states, a lane four of its sums: states i0, i0 + di,
+// ... of which the first is CTA c's slot 1 and the others the slots 0 of the
+// CTAs after it.
+template <int NT>
+__device__ __forceinline__ float4 kv8_join_column(const Kv8AttnArgs& a, int64_t c, int col, int i0, int di, int n, float& M,
+                                                  float& l) {
+    constexpr int kPart = kv8_part_floats<NT>();
+    const int lane = threadIdx.x & 31;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    M = -FLT_MAX;
+    l = 0.f;
+#pragma unroll 4
+    for (int i = i0; i < n; i += di) {
+        const float* p = a.part + (2 * (c + i) + (i == 0)) * kPart;
+        const float2 ml = *reinterpret_cast<const float2*>(p + 8 * NT * kD + 2 * col);
+        const float4 x = *reinterpret_cast<const float4*>(p + col * kD + 4 * lane);
+        const float m = fmaxf(M, ml.x), fa = ex2(M - m), fb = ex2(ml.x - m);
+        acc = make_float4(acc.x * fa + x.x * fb, acc.y * fa + x.y * fb, acc.z * fa + x.z * fb, acc.w * fa + x.w * fb);
+        l = l * fa + ml.y * fb;
+        M = m;
+    }
+    return acc;
+}
+
+// Joins the row that crosses the end of CTA c's range, if that row began
+// inside it.  gridDim.y == 1 (rows in few pieces): a warp takes whole columns;
+// else blockIdx.y is the column and every warp takes each eighth state.
 template <int NT, bool LIST>
 __global__ void __launch_bounds__(32 * kKv8Warps) kv8_join_kernel(Kv8AttnArgs a, int n_cta, int least) {
     Kv8Scan<NT, LIST> scan;
@@ -921,26 +945,28 @@ __global__ void __launch_bounds__(32 * kKv8Warps) kv8_join_kernel(Kv8AttnArgs a,
     if (w1 >= scan.total) return;
     const int r = (int)((w1 - q.base) / q.chunks);
     const int64_t begin = q.base + (int64_t)r * q.chunks, end = begin + q.chunks;
-    const int64_t orow = kv8_out_row<NT>(a, q, r % q.groups, r / q.groups, blockIdx.y);
-    if (begin == w1 || begin < w0 || orow < 0) return;
-    const int n = (int)((end - 1) / scan.per - c) + 1;  // states: CTA c's slot 1, the following CTAs' slots 0
+    if (begin == w1 || begin < w0) return;
+    const int n = (int)((end - 1) / scan.per - c) + 1;
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, cg = r % q.groups, g = r / q.groups;
+    if (gridDim.y == 1) {
+        for (int col = wid; col < 8 * NT; col += kKv8Warps) {
+            const int64_t orow = kv8_out_row<NT>(a, q, cg, g, col);
+            if (orow < 0) return;
+            float M, l;
+            const float4 x = kv8_join_column<NT>(a, c, col, 0, 1, n, M, l);
+            const bool any = l > 0.f || l != l;
+            const float f = any ? 1.f / l : 0.f;
+            reinterpret_cast<uint2*>(a.O + orow * kD)[lane] = make_uint2(pack_bf16x2(x.x * f, x.y * f), pack_bf16x2(x.z * f, x.w * f));
+            if (lane == 0 && a.lse) a.lse[orow] = any ? M - kKv8Head + log2f(l) : -CUDART_INF_F;
+        }
+        return;
+    }
+    const int64_t orow = kv8_out_row<NT>(a, q, cg, g, blockIdx.y);
+    if (orow < 0) return;
     __shared__ float4 s_acc[kKv8Warps][32];
     __shared__ float2 s_ml[kKv8Warps];
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, col = blockIdx.y;
-    constexpr int kPart = kv8_part_floats<NT>();
-    float M = -FLT_MAX, l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = wid; i < n; i += kKv8Warps) {
-        const float* p = a.part + (2 * (c + i) + (i == 0)) * kPart;
-        const float2 ml = *reinterpret_cast<const float2*>(p + 8 * NT * kD + 2 * col);
-        const float4 x = *reinterpret_cast<const float4*>(p + col * kD + 4 * lane);
-        const float m = fmaxf(M, ml.x), fa = ex2(M - m), fb = ex2(ml.x - m);
-        acc = make_float4(acc.x * fa + x.x * fb, acc.y * fa + x.y * fb, acc.z * fa + x.z * fb, acc.w * fa + x.w * fb);
-        l = l * fa + ml.y * fb;
-        M = m;
-    }
-    s_acc[wid][lane] = acc;
+    float M, l;
+    s_acc[wid][lane] = kv8_join_column<NT>(a, c, blockIdx.y, wid, kKv8Warps, n, M, l);
     if (lane == 0) s_ml[wid] = make_float2(M, l);
     __syncthreads();
     if (threadIdx.x >= kD) return;
@@ -1018,7 +1044,9 @@ static lsa_status launch_kv8_split(Kv8AttnArgs a, const Kv8Plan& p, int64_t n_se
     if ((s = check_launch("kv8_split_kernel")) != LSA_OK || p.rows_per_seq > 0) return s;
     // the join's own scan runs while the split kernel drains
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(n - 1, LIST || one_each ? a.G : 8 * NT);
+    // a row's pieces: about n over the rows; rows of up to 16 by whole columns
+    const bool few = n_seq * a.hkv * 16 >= n;
+    cfg.gridDim = dim3(n - 1, few ? 1 : LIST || one_each ? a.G : 8 * NT);
     cfg.blockDim = dim3(32 * kKv8Warps);
     cfg.stream = st;
     cudaLaunchAttribute at{};
