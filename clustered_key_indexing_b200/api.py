@@ -575,6 +575,8 @@ class KV8:
             raise ValueError(f"page: expected one of {KV8_PAGES}, got {page}")
         if n_pages < 1 or hkv < 1:
             raise ValueError("n_pages and hkv must be positive")
+        if torch.device(device).type != "cuda":
+            raise ValueError("LSA calls take CUDA tensors (there is no CPU implementation)")
         shape = (n_pages, hkv, page, 128)
         K, V = (torch.zeros(shape, dtype=torch.uint8, device=device).view(KV8_DTYPES[fmt]) for _ in range(2))
         self._wrap(K, V, torch.full((n_pages, hkv, 2), 2.0 ** -100, dtype=F32, device=device))
@@ -608,36 +610,35 @@ class KV8:
 
 
 def _on(dev, *ts):
+    """Every tensor lies on `dev`, a CUDA device."""
     for t in ts:
         if t is not None and t.device != dev:
+            if not t.is_cuda:
+                break
             raise ValueError(f"LSA calls take tensors of one device: got {t.device} beside {dev}")
+    else:
+        if dev.type == "cuda":
+            return
+    raise ValueError("LSA calls take CUDA tensors (there is no CPU implementation)")
 
 
-def _arg(t, name, dtype, dev, shape):
-    """An argument's dtype, shape (None entries match any size) and layout: a
-    dense tensor on the cache's device.  Returns its address (None for None)."""
+def _arg(t, name, dtype, shape):
+    """An argument's dtype, shape (None entries match any size) and layout.
+    Returns its address (None for None)."""
     if t is None:
         return None
     _spec(t, name, dtype, shape)
-    if not t.is_cuda:
-        raise ValueError("LSA calls take CUDA tensors (there is no CPU implementation)")
-    if t.device != dev:
-        raise ValueError(f"LSA calls take tensors of one device: got {name} on {t.device} beside {dev}")
     if not t.is_contiguous():
         raise ValueError("LSA calls take contiguous tensors")
     return t.data_ptr()
 
 
-def _rows(t, name, heads, dev):
+def _rows(t, name, heads):
     """A bf16 [n, heads, 128] tensor whose token rows are dense (their stride
     may be larger: a slice of a fused projection).  Returns its address and the
     elements between rows."""
     if t.dtype != BF16 or t.dim() != 3 or t.shape[2] != 128 or (heads is not None and t.shape[1] != heads):
         _spec(t, name, BF16, (None, heads, 128))
-    if not t.is_cuda:
-        raise ValueError("LSA calls take CUDA tensors (there is no CPU implementation)")
-    if t.device != dev:
-        raise ValueError(f"LSA calls take tensors of one device: got {name} on {t.device} beside {dev}")
     n, h, _ = t.shape
     dense = h * 128
     if t.is_contiguous():
@@ -673,18 +674,18 @@ def kv8_write(kv: KV8, K: torch.Tensor, V: torch.Tensor, table: torch.Tensor, st
     """lsa_kv8_write: new tokens' K/V rows [n, hkv, 128] bf16 into the pages of
     their sequences: sequence b's rows cu[b] .. cu[b + 1] - 1 (cu None: one
     token each) at positions start[b] on, in pages table[b]."""
-    dev = kv.device
-    pk, ldk = _rows(K, "K", kv.hkv, dev)
-    pv, ldv = _rows(V, "V", kv.hkv, dev)
+    pk, ldk = _rows(K, "K", kv.hkv)
+    pv, ldv = _rows(V, "V", kv.hkv)
     n = K.shape[0]
     if V.shape[0] != n:
         raise ValueError(f"V: expected shape {tuple(K.shape)}, got {tuple(V.shape)}")
-    pt = _arg(table, "table", I32, dev, (None, None))
+    pt = _arg(table, "table", I32, (None, None))
     n_seq, max_pages = table.shape
-    ps = _arg(start, "start", I32, dev, (n_seq,))
-    pc = _arg(cu, "cu", I32, dev, (n_seq + 1,))
+    ps = _arg(start, "start", I32, (n_seq,))
+    pc = _arg(cu, "cu", I32, (n_seq + 1,))
     if cu is None and n != n_seq:
         raise ValueError(f"K: without cu, expected one row for each of {n_seq} sequences, got {n}")
+    _on(kv.device, K, V, table, start, cu)
     _launch(kv, stream, "lsa_kv8_write",
             lambda s: lib().lsa_kv8_write(kv._ref, pk, ldk, pv, ldv, n, pc, ps, pt, n_seq, max_pages, s))
     return kv
@@ -728,17 +729,18 @@ def kv8_attn(Q: torch.Tensor, kv: KV8, table: torch.Tensor, lens: torch.Tensor, 
     (cu None: one each); lens counts the new tokens too.  Returns (O bf16
     [nq, hq, 128], lse fp32 [nq, hq], base 2)."""
     dev, L = kv.device, lib()
-    pq, ld = _rows(Q, "Q", None, dev)
+    pq, ld = _rows(Q, "Q", None)
     nq, hq, _ = Q.shape
-    pt = _arg(table, "table", I32, dev, (None, None))
+    pt = _arg(table, "table", I32, (None, None))
     n_seq, max_pages = table.shape
-    pl = _arg(lens, "lens", I32, dev, (n_seq,))
-    pc = _arg(cu, "cu", I32, dev, (n_seq + 1,))
-    _arg(O, "O", BF16, dev, (nq, hq, 128))
-    _arg(lse, "lse", F32, dev, (nq, hq))
-    _arg(ws, "ws", torch.uint8, dev, (None,))
+    pl = _arg(lens, "lens", I32, (n_seq,))
+    pc = _arg(cu, "cu", I32, (n_seq + 1,))
+    _arg(O, "O", BF16, (nq, hq, 128))
+    _arg(lse, "lse", F32, (nq, hq))
+    _arg(ws, "ws", torch.uint8, (None,))
     if cu is None and nq != n_seq:
         raise ValueError(f"Q: without cu, expected one row for each of {n_seq} sequences, got {nq}")
+    _on(dev, Q, table, lens, cu, O, lse, ws)
     O, lse, po, pe, pw, nw, made = _kv8_buffers(dev, nq, hq, O, lse, ws,
                                                 L.lsa_kv8_attn_workspace_bytes(kv._ref, nq, hq, cu is None, n_seq, max_pages,
                                                                                sinks, window))
@@ -755,18 +757,19 @@ def kv8_sparse_attn(Q: torch.Tensor, kv: KV8, table: torch.Tensor, lens: torch.T
     None: query i is sequence i's), -1 = padding.  Returns (O bf16
     [nq, hq, 128], lse fp32 [nq, hq], base 2)."""
     dev, L = kv.device, lib()
-    pq, ld = _rows(Q, "Q", None, dev)
+    pq, ld = _rows(Q, "Q", None)
     nq, hq, _ = Q.shape
-    pt = _arg(table, "table", I32, dev, (None, None))
+    pt = _arg(table, "table", I32, (None, None))
     n_seq, max_pages = table.shape
-    pl = _arg(lens, "lens", I32, dev, (n_seq,))
-    pi = _arg(idx, "idx", I32, dev, (nq, kv.hkv, None))
-    pb = _arg(seq, "seq", I32, dev, (nq,))
-    _arg(O, "O", BF16, dev, (nq, hq, 128))
-    _arg(lse, "lse", F32, dev, (nq, hq))
-    _arg(ws, "ws", torch.uint8, dev, (None,))
+    pl = _arg(lens, "lens", I32, (n_seq,))
+    pi = _arg(idx, "idx", I32, (nq, kv.hkv, None))
+    pb = _arg(seq, "seq", I32, (nq,))
+    _arg(O, "O", BF16, (nq, hq, 128))
+    _arg(lse, "lse", F32, (nq, hq))
+    _arg(ws, "ws", torch.uint8, (None,))
     if seq is None and nq != n_seq:
         raise ValueError(f"Q: without seq, expected one row for each of {n_seq} sequences, got {nq}")
+    _on(dev, Q, table, lens, idx, seq, O, lse, ws)
     n_idx = idx.shape[2]
     O, lse, po, pe, pw, nw, made = _kv8_buffers(dev, nq, hq, O, lse, ws,
                                                 L.lsa_kv8_sparse_attn_workspace_bytes(kv._ref, nq, hq, n_idx))

@@ -1146,8 +1146,8 @@ lsa_status lsa_kv8_sparse_attn(const lsa_kv8* kv, const uint16_t* Q, int64_t q_s
         return s;
     if (n_idx < 0) return set_error(LSA_EINVAL, "lsa_kv8_sparse_attn: n_idx < 0");
     if (n_idx > INT32_MAX - 128) return set_error(LSA_EUNSUPPORTED, "lsa_kv8_sparse_attn: n_idx beyond 2^31");
+    if (nq == 0) return LSA_OK;  // before seq is looked at: an empty array may have no address
     if (!seq && nq != n_seq) return set_error(LSA_EINVAL, "lsa_kv8_sparse_attn: without seq, nq must equal n_seq");
-    if (nq == 0) return LSA_OK;
     if (!idx && n_idx > 0) return set_error(LSA_EINVAL, "lsa_kv8_sparse_attn: idx is NULL");
     Kv8AttnArgs a = kv8_args(kv, Q, q_stride, nq, hq, table, lens, n_seq, max_pages, O, lse, ws);
     a.seq = seq; a.idx = idx; a.n_idx = n_idx;

@@ -300,3 +300,274 @@ def test_copy_pages(lsa, fmt, page, hkv, n):
         P[dst] = P[src]
     for g, w in zip(host(kv), (K, V, scale)):
         np.testing.assert_array_equal(g, w)
+
+
+def test_offsets_past_32_bits(lsa):
+    """Pages at the end of pools of more than 2^32 bytes."""
+    rng = np.random.default_rng(21)
+    hkv, page, n, n_pages = 8, 256, 700, 17000
+    k, v = (bf16(rng.standard_normal((n, hkv, 128)))[0] for _ in range(2))
+    q = bf16(rng.standard_normal((1, hkv * 2, 128)))[0]
+    idx = torch.from_numpy(rng.permutation(n)[None, None].repeat(hkv, 1).astype(np.int32)).cuda()
+    got = []
+    for size, table in ((3, [0, 1, 2]), (n_pages, [n_pages - 1, n_pages - 3, n_pages - 2])):
+        kv = lsa.KV8(size, hkv, page=page)
+        lsa.kv8_write(kv, k, v, i32([table]), i32([0]), cu=i32([0, n]))
+        if size > 3:
+            lsa.kv8_copy_pages(kv, [n_pages - 1], [n_pages - 5])
+            table = [n_pages - 5] + table[1:]
+        got.append(lsa.kv8_attn(q, kv, i32([table]), i32([n])) + lsa.kv8_sparse_attn(q, kv, i32([table]), i32([n]), idx))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    lsa.check_device_error()
+
+
+# ------------------------------------------------- streams, graphs, errors
+
+def small_case(lsa, rng, fmt="e4m3", wide=True):
+    lens, hkv, page = [300, 77, 5], 2, 32
+    kv, table = filled(lsa, rng, lens, hkv, page, fmt)
+    if wide:                                     # the stream form: rows of more than 48 chunks are possible
+        t = np.full((3, 200), -1, np.int32)
+        t[:, :table.shape[1]] = table
+        table = t
+    return kv, i32(table), i32(lens), torch.from_numpy(random_lists(rng, 3, hkv, 1700 if wide else 90, lens, [0, 1, 2])).cuda()
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_graphs_share_nothing(lsa, wide):
+    """Two captured graphs of the same calls, replayed in turn on two streams
+    and with an eager call between, each with inputs of its own."""
+    rng = np.random.default_rng(30)
+    kv, table, lens, idx = small_case(lsa, rng, wide=wide)
+    qs = [bf16(rng.standard_normal((3, 8, 128)))[0] for _ in range(3)]
+
+    def calls(q):
+        return lsa.kv8_attn(q, kv, table, lens) + lsa.kv8_sparse_attn(q, kv, table, lens, idx)
+
+    want = [calls(q) for q in qs]
+    graphs = []
+    for q in qs[:2]:
+        g = torch.cuda.CUDAGraph()
+        buf = q.clone()
+        with torch.cuda.graph(g):
+            out = calls(buf)
+        graphs.append((g, buf, out))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(3):
+        for s, (g, _, _) in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+        eager = calls(qs[2])
+        torch.cuda.synchronize()
+        for (_, _, out), w in zip(graphs + [(0, 0, eager)], want):
+            for x, y in zip(out, w):
+                assert torch.equal(x, y)
+    graphs[0][1].copy_(qs[1])                    # a replay takes what the buffer holds then
+    graphs[0][0].replay()
+    torch.cuda.synchronize()
+    for x, y in zip(graphs[0][2], want[1]):
+        assert torch.equal(x, y)
+
+
+def test_a_captured_decode_step(lsa):
+    """Write and attend in one graph: lens and start are read on replay."""
+    rng = np.random.default_rng(31)
+    kv, table = filled(lsa, rng, [70, 33], 2, 16, "int8")
+    table = i32(np.concatenate([table, np.full((2, 2), -1, np.int32)], 1))
+    own = lsa.KV8(40, 2, page=16, fmt="int8")    # a second pool for the eager calls
+    table2 = i32(np.arange(2 * table.shape[1]).reshape(2, -1))
+    for b in range(2):
+        for j in range(5):
+            if table[b, j] >= 0:
+                for x, y in ((own.K, kv.K), (own.V, kv.V), (own.scale, kv.scale)):
+                    x[table2[b, j]] = y[table[b, j]]
+    k, v, q = (bf16(rng.standard_normal((2, h, 128)))[0] for h in (2, 2, 8))
+    start, lens = i32([70, 33]), i32([71, 34])
+    before = [t.clone() for t in (kv.K.view(torch.uint8), kv.V.view(torch.uint8), kv.scale)]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        lsa.kv8_write(kv, k, v, table, start)
+        o, lse = lsa.kv8_attn(q, kv, table, lens)
+    for t, b in zip((kv.K.view(torch.uint8), kv.V.view(torch.uint8), kv.scale), before):
+        assert torch.equal(t, b)                 # a capture runs nothing
+    for step in range(4):
+        for t in (k, v, q):
+            t.copy_(bf16(rng.standard_normal(tuple(t.shape)) * 2.0 ** step)[0])
+        g.replay()
+        lsa.kv8_write(own, k, v, table2, start)
+        wo, wl = lsa.kv8_attn(q, own, table2, lens)
+        torch.cuda.synchronize()
+        assert torch.equal(o, wo) and torch.equal(lse, wl)
+        start += 1
+        lens += 1
+    lsa.check_device_error()
+
+
+def test_another_stream(lsa):
+    rng = np.random.default_rng(32)
+    kv, table, lens, idx = small_case(lsa, rng)
+    q = bf16(rng.standard_normal((3, 8, 128)))[0]
+    want = lsa.kv8_attn(q, kv, table, lens) + lsa.kv8_sparse_attn(q, kv, table, lens, idx)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = lsa.kv8_attn(q, kv, table, lens, stream=s) + lsa.kv8_sparse_attn(q, kv, table, lens, idx, stream=s)
+    junk = [torch.full((1 << 20,), float("nan"), device="cuda") for _ in range(8)]   # what the calls freed is not reused yet
+    torch.cuda.current_stream().wait_stream(s)
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)
+    del junk
+    O, lse = torch.empty(3, 8, 128, dtype=torch.bfloat16, device="cuda"), torch.empty(3, 8, device="cuda")
+    ws = torch.empty(lsa.kv8_attn_workspace_bytes(kv, 3, 8, 3, table.shape[1]), dtype=torch.uint8, device="cuda")
+    assert ws.numel() > 0
+    r = lsa.kv8_attn(q, kv, table, lens, O=O, lse=lse, ws=ws)
+    assert r[0] is O and r[1] is lse and torch.equal(O, want[0]) and torch.equal(lse, want[1])
+
+
+def test_bad_pages_and_ranges_are_reported(lsa):
+    from clustered_key_indexing_b200._lib import LSA_EDEVICE, LSAError
+
+    def reported(what):
+        torch.cuda.synchronize()
+        with pytest.raises(LSAError, match=what) as e:
+            lsa.check_device_error()
+        assert e.value.status == LSA_EDEVICE
+        lsa.check_device_error()
+
+    rng = np.random.default_rng(33)
+    kv, table, lens, idx = small_case(lsa, rng, wide=False)
+    K, V, scale = host(kv)
+    q, hq = bf16(rng.standard_normal((3, 8, 128)))
+    for bad in (-1, kv.n_pages, 2 ** 31 - 1):
+        t = table.clone()
+        t[0, 1] = bad                            # keys 32 .. 63 of the first sequence are skipped
+        o, lse = lsa.kv8_attn(q, kv, t, lens)
+        reported("page number outside")
+        k = [j for j in range(300) if not 32 <= j < 64]
+        want = ref.lists(hq, K, V, scale, table.cpu().numpy(), [300, 77, 5], [0, 1, 2],
+                         np.array([[k] * 2, [list(range(77)) + [-1] * (len(k) - 77)] * 2, [list(range(5)) + [-1] * (len(k) - 5)] * 2]), "e4m3")
+        close(o, want[0], want[2])
+        o, lse = lsa.kv8_sparse_attn(q, kv, t, lens, idx)
+        reported("page number outside")
+        ix = idx.cpu().numpy().copy()
+        ix[0][(ix[0] >= 32) & (ix[0] < 64)] = -1
+        want = ref.lists(hq, K, V, scale, table.cpu().numpy(), [300, 77, 5], [0, 1, 2], ix, "e4m3")
+        close(o, want[0], want[2])
+    over = idx.clone()
+    over[1, 0, 3] = 77                           # a position past its sequence
+    o, _ = lsa.kv8_sparse_attn(q, kv, table, lens, over)
+    reported("index entry")
+    over[1, 0, 3] = -1
+    assert torch.equal(o, lsa.kv8_sparse_attn(q, kv, table, lens, over)[0])
+    lsa.kv8_sparse_attn(q, kv, table, lens, idx, seq=i32([0, 3, -1]))
+    reported("range outside")
+    lsa.kv8_attn(q, kv, table, i32([300, table.shape[1] * 32 + 1, -4]))
+    reported("range outside")
+    for cu in ([0, 2, 1, 3], [0, 1, 2, 4], [-1, 1, 2, 3]):
+        lsa.kv8_attn(q, kv, table, lens, cu=i32(cu))
+        reported("range outside")
+    k = bf16(rng.standard_normal((3, 2, 128)))[0]
+    before = host(kv)
+    t = table.clone()
+    t[:, :] = kv.n_pages
+    lsa.kv8_write(kv, k, k, t, i32([300, 77, 5]))
+    reported("page number outside")
+    for start, cu in (([-1, -5, 320 + 32 * table.shape[1]], None), ([table.shape[1] * 32] * 3, None), ([0, 0, 0], [0, 4, 5, 6])):
+        lsa.kv8_write(kv, k, k, table, i32(start), cu=None if cu is None else i32(cu))
+        reported("range outside")
+        if cu is None:
+            for x, y in zip(host(kv), before):
+                np.testing.assert_array_equal(x, y)
+
+
+def test_empty_calls(lsa):
+    rng = np.random.default_rng(34)
+    kv, table, lens, idx = small_case(lsa, rng)
+    none = torch.empty(0, 8, 128, dtype=torch.bfloat16, device="cuda")
+    o, lse = lsa.kv8_attn(none, kv, table, lens, cu=i32([0, 0, 0, 0]))
+    assert o.shape == (0, 8, 128) and lse.shape == (0, 8)
+    o, lse = lsa.kv8_sparse_attn(none, kv, table, lens, idx[:0], seq=i32([]))
+    assert o.shape == (0, 8, 128) and lse.shape == (0, 8)
+    before = host(kv)
+    kz = none[:, :2]
+    lsa.kv8_write(kv, kz, kz, table, lens, cu=i32([0, 0, 0, 0]))
+    lsa.kv8_copy_pages(kv, [], [])
+    for x, y in zip(host(kv), before):
+        np.testing.assert_array_equal(x, y)
+    q = bf16(rng.standard_normal((3, 8, 128)))[0]
+    o, lse = lsa.kv8_attn(q, kv, table, i32([0, 0, 0]))
+    assert not o.any() and torch.isneginf(lse).all()
+    o, lse = lsa.kv8_sparse_attn(q, kv, table, lens, torch.full_like(idx, -1))
+    assert not o.any() and torch.isneginf(lse).all()
+    o, lse = lsa.kv8_attn(q, kv, table[:, :0].contiguous(), i32([0, 0, 0]))
+    assert not o.any() and torch.isneginf(lse).all()
+    lsa.check_device_error()
+
+
+def test_results_do_not_depend_on_the_run(lsa):
+    rng = np.random.default_rng(35)
+    kv, table, lens, idx = small_case(lsa, rng)
+    q = bf16(rng.standard_normal((3, 8, 128)))[0]
+    first = lsa.kv8_attn(q, kv, table, lens) + lsa.kv8_sparse_attn(q, kv, table, lens, idx)
+    for _ in range(5):
+        for x, y in zip(lsa.kv8_attn(q, kv, table, lens) + lsa.kv8_sparse_attn(q, kv, table, lens, idx), first):
+            assert torch.equal(x, y)
+
+
+# ---------------------------------------------------------- as they are used
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_a_layer_over_the_cache(lsa, fmt):
+    """A prompt written into pages, selected and attended in chunks, then
+    decoded: appends, a fork, drafts that are partly rejected, a compaction."""
+    rng = np.random.default_rng(40)
+    T, hkv, hq, page = 2048, 2, 8, 64
+    cfg = lsa.Config(k=256, sinks=4, window=128)
+    W = torch.linalg.qr(torch.from_numpy(rng.standard_normal((128, 64))))[0].float().contiguous().cuda()
+    (K, hK), (V, hV), (Q, hQ) = (bf16(rng.standard_normal((T + 40, h, 128))) for h in (hkv, hkv, hq))
+    pages = lsa.KV8Pages(lsa.KV8(90, hkv, page=page, fmt=fmt))
+    hole, a = pages.add(), pages.add()
+    pages.append([hole], K[:100], V[:100], [100])
+    pages.append([a], K[:T], V[:T], [T])
+    # the prompt: index rows from the bf16 keys, attention over the codes
+    cache = lsa.Cache(hkv, T, cfg)
+    lsa.build_buckets(K[:T], W, cfg, cache)
+    table, lens = pages.table([a])
+    for t0, nq in ((0, 300), (T - 64, 64)):
+        idx = lsa.select(Q[t0:t0 + nq], t0, W, cache, cfg)
+        o, lse = lsa.kv8_sparse_attn(Q[t0:t0 + nq], pages.kv, table, lens, idx, seq=i32([0] * nq))
+        some = rng.permutation(nq)[:12]
+        wo, wl, to, tl = ref.lists(hQ[t0:t0 + nq][some], *host(pages.kv), table.cpu().numpy(), [T], [0] * 12, idx.cpu().numpy()[some], fmt)
+        close(o[torch.from_numpy(some).cuda()], wo, to)
+        close(lse[torch.from_numpy(some).cuda()], wl, tl)
+        # near the bf16 attention: the codes' relative error, averaged over the keys
+        full = lsa.sparse_attn(Q[t0:t0 + nq], K[:T], V[:T], idx).float()
+        assert (o.float() - full).norm() < 0.1 * full.norm()
+    # decode: one token, a fork, five drafts each of which two are kept
+    pages.append([a], K[T:T + 1], V[T:T + 1])
+    b = pages.fork(a)
+    used = pages.used_pages
+    pages.append([a, b], torch.cat([K[T + 1:T + 6], K[T + 11:T + 16]]), torch.cat([V[T + 1:T + 6], V[T + 11:T + 16]]), [5, 5])
+    assert pages.used_pages == used + 1          # the open page, copied once
+    qd, hqd = Q[T:T + 10], hQ[T:T + 10]
+
+    def attend(n):
+        table, lens = pages.table([a, b])
+        got = lsa.kv8_attn(qd[:2 * n], pages.kv, table, lens, cu=i32([0, n, 2 * n]), sinks=4, window=128)
+        want = ref.attn(hqd[:2 * n], *host(pages.kv), table.cpu().numpy(), lens.tolist(), [0, n, 2 * n], fmt, 4, 128)
+        close(got[0], want[0], want[2])
+        close(got[1], want[1], want[3])
+        return got
+
+    attend(5)
+    for s in (a, b):
+        pages.truncate(s, T + 3)
+    pages.append([b, a], K[T + 20:T + 22], V[T + 20:T + 22])
+    before = attend(2)
+    pages.free(hole)
+    assert pages.compact() > 0
+    after = attend(2)
+    assert torch.equal(before[0], after[0]) and torch.equal(before[1], after[1])
+    assert pages.used_pages == len(set(pages.pages(a)) | set(pages.pages(b))) == max(pages.pages(a) + pages.pages(b)) + 1
+    lsa.check_device_error()
