@@ -42,14 +42,15 @@ class lsa_tree(ctypes.Structure):
 MAX_BATCH = 128
 
 
+class lsa_kv8(ctypes.Structure):
+    _fields_ = [("fmt", i32), ("hkv", i32), ("page", i32), ("n_pages", i64), ("K", vp), ("V", vp), ("scale", vp)]
+
+
 class lsa_decode(ctypes.Structure):
     _fields_ = [("batch", i32), ("hkv", i32), ("hq", i32), ("cap", i64), ("K", vp), ("V", vp),
                 ("U_blk", vp), ("cache", lsa_cache), ("tree", lsa_tree), ("len", i64 * MAX_BATCH),
-                ("K_shared", vp), ("V_shared", vp), ("shared_len", i64)]
-
-
-class lsa_kv8(ctypes.Structure):
-    _fields_ = [("fmt", i32), ("hkv", i32), ("page", i32), ("n_pages", i64), ("K", vp), ("V", vp), ("scale", vp)]
+                ("K_shared", vp), ("V_shared", vp), ("shared_len", i64), ("kv8", ctypes.POINTER(lsa_kv8)),
+                ("kv8_table", vp), ("kv8_max_pages", i32)]
 
 
 class LSAError(RuntimeError):

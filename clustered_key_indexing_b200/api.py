@@ -386,12 +386,17 @@ class Decode:
     (request, kv-head) pairs, the per-request block ring, and (tree mode) the
     tree.  `load` installs a prompt, `step` decodes one token per request."""
 
+    kv8 = None
+
     def __init__(self, batch: int, hkv: int, hq: int, cap: int, cfg: Config, device="cuda", shared=None,
-                 fp8: bool = False):
+                 fp8: bool = False, kv8=None, kv8_table=None):
         """`shared`: optional (K_shared, V_shared) [shared_len, hkv, 128], a
         prefix every request starts with (shared_len a multiple of 512); the
         pools then hold each request's tokens from shared_len on.  `fp8`: the
-        cache keeps FP8 centroids and the flat search scores those."""
+        cache keeps FP8 centroids and the flat search scores those.  `kv8`: keep
+        the keys and values in 8 bits, in the pages of a KV8 that kv8_table
+        [batch, cap / page] names (the caller's, which it may rewrite between
+        calls), or, given a format ("e4m3", "int8"), in a KV8 of its own."""
         if cap % 512:
             raise ValueError("cap must be a multiple of 512")
         self.cfg = cfg
@@ -399,14 +404,38 @@ class Decode:
         self.shared = shared
         sl = 0 if shared is None else int(shared[0].shape[0])
         self.shared_len = sl
-        self.K = torch.zeros((batch, cap - sl, hkv, 128), dtype=torch.bfloat16, **z)
-        self.V = torch.zeros((batch, cap - sl, hkv, 128), dtype=torch.bfloat16, **z)
+        if kv8 is None:
+            if kv8_table is not None:
+                raise ValueError("kv8_table: needs kv8")
+            self.K = torch.zeros((batch, cap - sl, hkv, 128), dtype=torch.bfloat16, **z)
+            self.V = torch.zeros((batch, cap - sl, hkv, 128), dtype=torch.bfloat16, **z)
+        else:
+            if shared is not None:
+                raise ValueError("shared: with kv8 a prefix is shared through the page table")
+            if isinstance(kv8, str):
+                if kv8_table is not None:
+                    raise ValueError("kv8_table: a cache of the state's own has its own table")
+                kv8 = KV8(batch * cap // 64, hkv, page=64, fmt=kv8, device=device)
+                kv8_table = torch.arange(kv8.n_pages, dtype=torch.int32, device=kv8.device).view(batch, -1)
+            elif kv8_table is None:
+                raise ValueError("kv8_table: a cache of the caller's needs one")
+            if kv8.hkv != hkv:
+                raise ValueError(f"kv8: expected {hkv} kv-heads, got {kv8.hkv}")
+            _arg(kv8_table, "kv8_table", I32, (batch, None))
+            _on(kv8.device, kv8_table)
+            if kv8_table.shape[1] * kv8.page < cap:
+                raise ValueError(f"kv8_table: {kv8_table.shape[1]} pages of {kv8.page} do not hold {cap} tokens")
+        self.kv8, self.kv8_table = kv8, kv8_table
         self.U_blk = torch.zeros((batch * hkv, 128, 64), dtype=torch.float64, **z)
         self.cache = Cache(batch * hkv, cap, cfg, device=device, with_units=False, fp8=fp8)
         self.tree = Tree(self.cache, device=device) if cfg.mode == 1 else None
         d = _lib.lsa_decode()
         d.batch, d.hkv, d.hq, d.cap = batch, hkv, hq, cap
-        d.K, d.V, d.U_blk = self.K.data_ptr(), self.V.data_ptr(), self.U_blk.data_ptr()
+        d.U_blk = self.U_blk.data_ptr()
+        if kv8 is None:
+            d.K, d.V = self.K.data_ptr(), self.V.data_ptr()
+        else:
+            d.kv8, d.kv8_table, d.kv8_max_pages = ctypes.pointer(kv8.c), kv8_table.data_ptr(), kv8_table.shape[1]
         if shared is not None:
             _spec(shared[0], "K_shared", BF16, (None, hkv, 128))
             _spec(shared[1], "V_shared", BF16, tuple(shared[0].shape))
@@ -425,20 +454,30 @@ class Decode:
     def len(self):
         return [int(self.d.len[i]) for i in range(self.d.batch)]
 
-    def load(self, r: int, K: torch.Tensor, V: torch.Tensor, W_k: torch.Tensor, stream=None):
+    def load(self, r: int, K: torch.Tensor, V: torch.Tensor, W_k: torch.Tensor, stream=None, written: bool = False):
         """Install a prompt as request r: K/V [n, hkv, 128], or with a shared
-        prefix the prompt's tokens after it (the prompt holds shared_len + n)."""
-        hkv = self.K.shape[2]
+        prefix the prompt's tokens after it (the prompt holds shared_len + n).
+        written (kv8 only): the pages hold the prompt's codes already."""
+        hkv = self.K.shape[2] if self.kv8 is None else self.kv8.hkv
         _spec(K, "K", BF16, (None, hkv, 128))
         _spec(V, "V", BF16, tuple(K.shape))
         _spec(W_k, "W_k", F32, W_SHAPE)
         _need_cuda(W_k)
         n = K.shape[0]
-        self.K[r, :n].copy_(K)
-        self.V[r, :n].copy_(V)
+        if self.kv8 is None:
+            if written:
+                raise ValueError("written: the state keeps no 8-bit pages")
+            self.K[r, :n].copy_(K)
+            self.V[r, :n].copy_(V)
+        else:
+            _need_cuda(K, V)
+            _on(self.kv8.device, K, V, W_k)
+            self.d.K, self.d.V = K.data_ptr() or None, None if written else V.data_ptr() or None
         check(lib().lsa_decode_load(ctypes.byref(self.d), r, self.shared_len + n, _ptr(W_k),
                                     ctypes.byref(self.cfg.c()), _ptr(self.ws), self.ws.numel(), _stream(stream)),
               "lsa_decode_load")
+        if self.kv8 is not None:
+            self.d.K = self.d.V = None  # the prompt was only read
 
     def step(self, q, k, v, W_k, W_q, o=None, idx_out=None, stream=None):
         """One token per request: q [batch, hq, 128], k/v [batch, hkv, 128]."""

@@ -49,6 +49,9 @@ lsa_status launch_attn(const uint16_t* Q, const uint16_t* K, const uint16_t* V, 
                        int64_t nq, int32_t hq, int32_t hkv, int32_t n_idx, int64_t T, uint16_t* O,
                        cudaStream_t st, int64_t kv_q_stride, int split, int32_t n_use, const float* Ow,
                        const float* lse, const uint16_t* Ks, const uint16_t* Vs, int64_t shared_len);
+static lsa_status check_kv8(const lsa_kv8* c);
+lsa_status launch_kv8_prompt(const lsa_kv8* kv, const uint16_t* K, const uint16_t* V, int64_t n, const int32_t* table,
+                             int32_t max_pages, cudaStream_t st);
 
 // ------------------------------------------------------------- key latent
 
@@ -78,8 +81,10 @@ constexpr int kDecBins = 2048;       // histogram bins over the row's score rang
 struct AppendArgs {
     const uint16_t* k;   // [batch, hkv, 128] new keys
     const uint16_t* v;   // [batch, hkv, 128] new values
-    uint16_t* K;         // [batch, tail, hkv, 128] (tail = cap - shared_len)
+    uint16_t* K;         // [batch, tail, hkv, 128] (tail = cap - shared_len); NULL: paged 8-bit keys and values ...
     uint16_t* V;
+    int32_t* start;      // ... whose calls read the positions and lengths [batch] written here
+    int32_t* lens;
     const float* W;      // W_k [128, 64]
     double* U_blk;       // [batch * hkv, 128, 64]
     int64_t tail, shared_len;
@@ -104,7 +109,12 @@ __global__ void __launch_bounds__(256) decode_append_kernel(AppendArgs a) {
     const uint16_t* ks = a.k + w * kD;
     const uint16_t* vs = a.v + w * kD;
     const int64_t dst = ((r * a.tail + (t - a.shared_len)) * a.hkv + h) * kD;
-    if (lane < 16) {
+    if (a.K == nullptr) {
+        if (h == 0 && lane == 0) {
+            a.start[r] = (int32_t)t;
+            a.lens[r] = (int32_t)(t + 1);
+        }
+    } else if (lane < 16) {
         reinterpret_cast<uint4*>(a.K + dst)[lane] = reinterpret_cast<const uint4*>(ks)[lane];
         reinterpret_cast<uint4*>(a.V + dst)[lane] = reinterpret_cast<const uint4*>(vs)[lane];
     }
@@ -792,6 +802,10 @@ struct DecodeWs {
     int32_t* seg;
     int32_t* segn;
     int64_t nch;
+    int32_t* start;   // paged 8-bit keys and values: positions, lengths, the attention's workspace
+    int32_t* lens;
+    char* kv8_ws;
+    size_t kv8_ws_bytes;
     double* Utmp;
     size_t step_bytes, load_bytes;
 };
@@ -814,6 +828,12 @@ static DecodeWs carve_decode(const lsa_cfg* cfg, const lsa_decode* d, char* base
         w.tot = (unsigned long long*)take((size_t)rows * 8);
         w.seg = (int32_t*)take((size_t)rows * w.nch * kCap * 4);
         w.segn = (int32_t*)take((size_t)rows * w.nch * 4);
+    }
+    if (d->kv8) {
+        w.start = (int32_t*)take((size_t)d->batch * 4);
+        w.lens = (int32_t*)take((size_t)d->batch * 4);
+        w.kv8_ws_bytes = lsa_kv8_sparse_attn_workspace_bytes(d->kv8, d->batch, d->hq, (int32_t)decode_row_len(cfg));
+        w.kv8_ws = take(w.kv8_ws_bytes);
     }
     w.step_bytes = o;
     // a request load reuses the same bytes for its temporary pooled units
@@ -856,7 +876,16 @@ static lsa_status check_decode(const lsa_decode* d, const lsa_cfg* cfg) {
     const int G = d->hq / d->hkv;
     if (G != 1 && G != 2 && G != 4 && G != 8) return set_error(LSA_EUNSUPPORTED, "decode: hq / hkv must be 1, 2, 4 or 8");
     if (d->cap < kBlockKeys || d->cap % kBlockKeys) return set_error(LSA_EINVAL, "decode: cap must be a positive multiple of 512");
-    if (!d->K || !d->V || !d->U_blk) return set_error(LSA_EINVAL, "decode: K, V or U_blk is NULL");
+    if (!d->U_blk || (!d->kv8 && (!d->K || !d->V))) return set_error(LSA_EINVAL, "decode: K, V or U_blk is NULL");
+    if (d->kv8) {
+        const lsa_status s = check_kv8(d->kv8);
+        if (s != LSA_OK) return s;
+        if (d->kv8->hkv != d->hkv) return set_error(LSA_EINVAL, "decode: kv8->hkv must equal hkv");
+        if (d->shared_len != 0) return set_error(LSA_EINVAL, "decode: with kv8 a prefix is shared through the page table");
+        if (!d->kv8_table || (int64_t)d->kv8_max_pages * d->kv8->page < d->cap)
+            return set_error(LSA_EINVAL, "decode: kv8_table must hold cap tokens a request");
+        if (d->cap > INT32_MAX - 512) return set_error(LSA_EUNSUPPORTED, "decode: cap beyond 2^31");
+    }
     if (d->shared_len < 0 || d->shared_len % kBlockKeys || d->shared_len >= d->cap)
         return set_error(LSA_EINVAL, "decode: shared_len must be a multiple of 512 in [0, cap)");
     if (d->shared_len > 0 && (!d->K_shared || !d->V_shared))
@@ -930,7 +959,14 @@ lsa_status lsa_decode_load(lsa_decode* d, int32_t r, int64_t n, const float* W_k
     cudaStream_t st = (cudaStream_t)stream;
     const lsa_cache view = request_view(d, r);
     const int64_t sl = d->shared_len;
-    const uint16_t* Kr = d->K + (int64_t)r * (d->cap - sl) * d->hkv * kD;   // the request's rows from sl on
+    const uint16_t* Kr = d->kv8 ? d->K : d->K + (int64_t)r * (d->cap - sl) * d->hkv * kD;  // the request's rows from sl on
+    if (d->kv8) {
+        if (!d->K && n > 0) return set_error(LSA_EINVAL, "lsa_decode_load: K must hold the prompt's rows");
+        if (((uintptr_t)d->K | (uintptr_t)d->V) & 15u) return set_error(LSA_EINVAL, "lsa_decode_load: K and V must be 16-byte aligned");
+        if (d->V && (s = launch_kv8_prompt(d->kv8, d->K, d->V, n, d->kv8_table + (int64_t)r * d->kv8_max_pages,
+                                           d->kv8_max_pages, st)) != LSA_OK)
+            return s;
+    }
     const int64_t nb = n / kBlockKeys, nc = nb * kBlockKeys;                 // nc >= sl (sl is whole blocks)
     if (nb > 0) {
         if (sl > 0 &&
@@ -968,14 +1004,17 @@ lsa_status lsa_decode_step(lsa_decode* d, const uint16_t* q, const uint16_t* k, 
         if (d->len[r] < 0 || d->len[r] >= d->cap)
             return set_error(LSA_ENOSPACE, "lsa_decode_step: request %d is full (len %lld, cap %lld)", r,
                              (long long)d->len[r], (long long)d->cap);
+    if (d->kv8 && (((uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)o) & 15u))
+        return set_error(LSA_EINVAL, "lsa_decode_step: q, k, v and o must be 16-byte aligned");
     const DecodeWs w = carve_decode(cfg, d, (char*)ws);
     if (ws_bytes < w.step_bytes) return set_error(LSA_ENOSPACE, "lsa_decode_step: workspace too small");
+    if (d->kv8 && ((uintptr_t)w.kv8_ws & 15u)) return set_error(LSA_EINVAL, "lsa_decode_step: ws must be 16-byte aligned");
     cudaStream_t st = (cudaStream_t)stream;
     const int64_t rows = (int64_t)d->batch * d->hkv;
 
     // (1) append k/v and pool the new key
     AppendArgs ap{};
-    ap.k = k; ap.v = v; ap.K = d->K; ap.V = d->V; ap.W = W_k; ap.U_blk = d->U_blk;
+    ap.k = k; ap.v = v; ap.K = d->kv8 ? nullptr : d->K; ap.V = d->V; ap.start = w.start; ap.lens = w.lens; ap.W = W_k; ap.U_blk = d->U_blk;
     ap.tail = d->cap - d->shared_len; ap.shared_len = d->shared_len;
     ap.hkv = d->hkv; ap.batch = d->batch;
     ap.hist = cfg->mode == 0 ? w.hist : nullptr;
@@ -986,6 +1025,9 @@ lsa_status lsa_decode_step(lsa_decode* d, const uint16_t* q, const uint16_t* k, 
         decode_append_kernel<<<(unsigned)ceil_div<int64_t>(rows, 8), 256, 0, st>>>(ap);
     }
     if ((s = check_launch("decode_append_kernel")) != LSA_OK) return s;
+    if (d->kv8 && (s = lsa_kv8_write(d->kv8, k, (int64_t)d->hkv * kD, v, (int64_t)d->hkv * kD, d->batch, nullptr, w.start,
+                                     d->kv8_table, d->batch, d->kv8_max_pages, stream)) != LSA_OK)
+        return s;
 
     // (2) cluster every block this token completed
     int32_t head0[LSA_MAX_BATCH];
@@ -1067,6 +1109,10 @@ lsa_status lsa_decode_step(lsa_decode* d, const uint16_t* q, const uint16_t* k, 
         if ((s = check_launch("decode_resolve_kernel")) != LSA_OK) return s;
     }
     // (4) attention: each request reads its own K/V rows
+    if (d->kv8)
+        return lsa_kv8_sparse_attn(d->kv8, q, (int64_t)d->hq * kD, d->batch, d->hq, nullptr, d->kv8_table, w.lens, d->batch,
+                                   d->kv8_max_pages, idx, (int32_t)decode_row_len(cfg), o, nullptr, w.kv8_ws,
+                                   w.kv8_ws_bytes, stream);
     return launch_attn(q, d->K, d->V, idx, d->batch, d->hq, d->hkv, (int32_t)decode_row_len(cfg), d->cap,
                        o, st, d->cap - d->shared_len, 8, -1, nullptr, nullptr, d->K_shared, d->V_shared,
                        d->shared_len);

@@ -72,7 +72,7 @@ struct Kv8WriteArgs {
     uint8_t* Vp;
     float* scale;            // [n_pages, hkv, 2]
     const int32_t* cu;       // [n_seq + 1], NULL: one token per sequence
-    const int32_t* start;    // [n_seq]
+    const int32_t* start;    // [n_seq], NULL: one sequence, all n_tokens from position 0 on
     const int32_t* table;    // [n_seq, max_pages]
     int64_t n_tokens, n_pages;
     int32_t n_seq, max_pages, hkv;
@@ -84,8 +84,8 @@ struct Kv8WriteArgs {
 __device__ __forceinline__ void kv8_new_tokens(const Kv8WriteArgs& a, int b, int page, int64_t& q0, int64_t& n,
                                                int64_t& s0) {
     q0 = a.cu ? a.cu[b] : b;
-    n = a.cu ? (int64_t)a.cu[b + 1] - q0 : 1;
-    s0 = a.start[b];
+    n = a.cu ? (int64_t)a.cu[b + 1] - q0 : a.start ? 1 : a.n_tokens;
+    s0 = a.start ? a.start[b] : 0;
     if (n == 0) return;
     if (q0 < 0 || n < 0 || q0 + n > a.n_tokens || s0 < 0 || s0 + n > (int64_t)a.max_pages * page) {
         raise_device_error(kErrKv8Range);
@@ -110,12 +110,13 @@ __global__ void __launch_bounds__(256) kv8_write_kernel(Kv8WriteArgs a) {
     const int64_t item = blockIdx.x / a.hkv;
     const int h = blockIdx.x % a.hkv;
     if (wid == 0) {
-        if (a.cu == nullptr) {  // one token per sequence: touched page number b is sequence b's
+        if (a.cu == nullptr) {  // one token per sequence (touched page b is sequence b's) or one sequence's first pages
             if (lane == 0) {
+                const int b = a.start ? (int)item : 0;
                 int64_t q0, n, s0;
-                kv8_new_tokens(a, (int)item, page, q0, n, s0);
-                s_seq = n > 0 ? (int32_t)item : -1;
-                s_at[0] = s0; s_at[1] = s0 + n; s_at[2] = q0; s_at[3] = s0 / page;
+                kv8_new_tokens(a, b, page, q0, n, s0);
+                s_seq = n > 0 ? b : -1;
+                s_at[0] = s0; s_at[1] = s0 + n; s_at[2] = q0; s_at[3] = a.start ? s0 / page : item;
             }
         } else {
             if (lane == 0) s_seq = -1;
@@ -283,6 +284,27 @@ static void launch_kv8_write(const Kv8WriteArgs& a, int page, dim3 grid, cudaStr
     }
 }
 
+static lsa_status run_kv8_write(const lsa_kv8* kv, const Kv8WriteArgs& a, int64_t items, cudaStream_t st) {
+    {
+        KTime kt_("kv8_write_kernel", st);
+        const dim3 grid((unsigned)(items * kv->hkv), kv->page <= 64 ? 1 : 2);
+        if (kv->fmt == LSA_KV8_E4M3) launch_kv8_write<0>(a, kv->page, grid, st);
+        else launch_kv8_write<1>(a, kv->page, grid, st);
+    }
+    return check_launch("kv8_write_kernel");
+}
+
+// A whole prompt into one sequence's pages (decode's load).
+lsa_status launch_kv8_prompt(const lsa_kv8* kv, const uint16_t* K, const uint16_t* V, int64_t n, const int32_t* table,
+                             int32_t max_pages, cudaStream_t st) {
+    if (n <= 0) return LSA_OK;
+    Kv8WriteArgs a{};
+    a.K = K; a.V = V; a.k_stride = a.v_stride = (int64_t)kv->hkv * kD;
+    a.Kp = kv->K; a.Vp = kv->V; a.scale = kv->scale;
+    a.table = table; a.n_tokens = n; a.n_pages = kv->n_pages; a.n_seq = 1; a.max_pages = max_pages; a.hkv = kv->hkv;
+    return run_kv8_write(kv, a, ceil_div<int64_t>(n, kv->page), st);
+}
+
 template <int N>
 static void launch_kv8_copy(const lsa_kv8* c, const int32_t* src, const int32_t* dst, int n, cudaStream_t st) {
     Kv8Pairs<N> p;
@@ -317,14 +339,7 @@ lsa_status lsa_kv8_write(const lsa_kv8* kv, const uint16_t* K, int64_t k_stride,
     a.Kp = kv->K; a.Vp = kv->V; a.scale = kv->scale;
     a.cu = cu; a.start = start; a.table = table; a.n_tokens = n_tokens; a.n_pages = kv->n_pages;
     a.n_seq = n_seq; a.max_pages = max_pages; a.hkv = kv->hkv;
-    const cudaStream_t st = (cudaStream_t)stream;
-    {
-        KTime kt_("kv8_write_kernel", st);
-        const dim3 grid((unsigned)(items * kv->hkv), kv->page <= 64 ? 1 : 2);
-        if (kv->fmt == LSA_KV8_E4M3) launch_kv8_write<0>(a, kv->page, grid, st);
-        else launch_kv8_write<1>(a, kv->page, grid, st);
-    }
-    return check_launch("kv8_write_kernel");
+    return run_kv8_write(kv, a, items, (cudaStream_t)stream);
 }
 
 lsa_status lsa_kv8_copy_pages(const lsa_kv8* kv, const int32_t* src, const int32_t* dst, int64_t n, void* stream) {

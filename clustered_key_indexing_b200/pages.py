@@ -10,12 +10,13 @@ to move.  The calls are taken from an `ops` object, as in `seqshard`, so that
 the tests run the same logic without a GPU.
 
 Nothing changes when a call is refused: the pages and copies of an append are
-planned first, then the device calls are made, then the tables change.  Device
+planned first, then the device calls are made, then the sequences change.  Device
 work is ordered by the stream of each call: use one stream, or order them.
 """
 from __future__ import annotations
 
 import heapq
+import itertools
 
 import torch
 
@@ -134,76 +135,105 @@ class KV8Pages:
         self._release(seq.pages[keep:])
         seq.pages, seq.len = seq.pages[:keep], n
 
-    def append(self, sids, K, V, counts=None, stream=None):
-        """Write new tokens: K, V [n, hkv, 128] bf16, counts[i] rows for
-        sequence sids[i] (default one each), in order.  LSA_ENOSPACE if the free
-        pages do not suffice."""
+    def _counts(self, what, sids, counts):
         sids = list(sids)
         seqs = [self._seq(s) for s in sids]
         if len(set(sids)) < len(sids):
-            raise ValueError("append: a sequence stands twice")
+            raise ValueError(f"{what}: a sequence stands twice")
         counts = [1] * len(sids) if counts is None else [int(c) for c in counts]
         if len(counts) != len(sids) or any(c < 0 for c in counts):
-            raise ValueError("append: counts must be one non-negative number a sequence")
-        shape = (sum(counts), self.kv.hkv, 128)
-        for name, t in (("K", K), ("V", V)):
-            if tuple(t.shape) != shape:
-                raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
-            if t.dtype != torch.bfloat16:
-                raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
+            raise ValueError(f"{what}: counts must be one non-negative number a sequence")
+        return seqs, counts
+
+    def _own(self, what, seqs, counts, stream, then=None):
+        """Give every sequence pages of its own for its next tokens: a copy of
+        a shared open page, new pages behind it; then run `then(tables)`.  What
+        the sequences hold changes only when all of it has been done."""
         page = self.kv.page
-        # plan: own the open page, then add pages behind it
-        refs: dict[int, int] = {}       # references that this call gives up
+        given: dict[int, int] = {}      # references to shared pages that are given up
         copies: list[tuple[int, int]] = []
-        tables, short = [], 0
-        taken: list[int] = []
-
-        def take():
-            nonlocal short
-            if not self._free:
-                short += 1
-                return -1
-            taken.append(heapq.heappop(self._free))
-            return taken[-1]
-
+        tables, taken, short = [], [], 0
         for seq, c in zip(seqs, counts):
             pages = list(seq.pages)
+            want = [None] * max(0, -(-(seq.len + c) // page) - len(pages))
             if c > 0 and seq.len % page:
-                p = pages[-1]
-                if self.refs[p] - refs.get(p, 0) > 1:
-                    refs[p] = refs.get(p, 0) + 1
-                    pages[-1] = take()
-                    copies.append((p, pages[-1]))
-            pages += [take() for _ in range(-(-(seq.len + c) // page) - len(pages))]
+                at = seq.len // page
+                p = pages[at]
+                if self.refs[p] - given.get(p, 0) > 1:
+                    given[p] = given.get(p, 0) + 1
+                    pages[at] = None
+            pages += want
+            for i, p in enumerate(pages):
+                if p is not None:
+                    continue
+                if self._free:
+                    pages[i] = heapq.heappop(self._free)
+                    taken.append(pages[i])
+                    if i < len(seq.pages):
+                        copies.append((seq.pages[i], pages[i]))
+                else:
+                    short += 1
             tables.append(pages)
         try:
             if short:
-                raise LSAError(LSA_ENOSPACE, f"append: {short} more free pages are needed than the {len(taken)} there are")
-            if shape[0]:
-                if copies:
-                    self.ops.copy(self.kv, [s for s, _ in copies], [d for _, d in copies], stream)
-                width = max(len(p) for p in tables)
-                up = stream if stream is not None and self.kv.device.type == "cuda" else None
-                with torch.cuda.stream(up):  # the tables are uploaded where they are read
-                    table = self._upload([p + [-1] * (width - len(p)) for p in tables]).view(len(tables), width)
-                    start = self._upload([s.len for s in seqs])
-                    cu = None
-                    if any(c != 1 for c in counts):
-                        ends = [0]
-                        for c in counts:
-                            ends.append(ends[-1] + c)
-                        cu = self._upload(ends)
-                    self.ops.write(self.kv, K, V, table, start, cu, stream)
+                raise LSAError(LSA_ENOSPACE, f"{what}: {short} more free pages are needed than the {len(taken)} there are")
+            if copies:
+                self.ops.copy(self.kv, [s for s, _ in copies], [d for _, d in copies], stream)
+            if then is not None:
+                then(tables)
         except BaseException:
             for p in taken:
                 heapq.heappush(self._free, p)
             raise
         for p in taken:
             self.refs[p] = 1
-        for p, n in refs.items():
+        for p, n in given.items():
             self.refs[p] -= n
-        for seq, pages, c in zip(seqs, tables, counts):
-            seq.pages, seq.len = pages, seq.len + c
+        for seq, pages in zip(seqs, tables):
+            seq.pages = pages
+
+    def append(self, sids, K, V, counts=None, stream=None):
+        """Write new tokens: K, V [n, hkv, 128] bf16, counts[i] rows for
+        sequence sids[i] (default one each), in order.  LSA_ENOSPACE if the free
+        pages do not suffice."""
+        seqs, counts = self._counts("append", sids, counts)
+        shape = (sum(counts), self.kv.hkv, 128)
+        for name, t in (("K", K), ("V", V)):
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+            if t.dtype != torch.bfloat16:
+                raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
+
+        def write(tables):
+            width = max(len(p) for p in tables)
+            up = stream if self.kv.device.type == "cuda" else None
+            with torch.cuda.stream(up):  # the tables are uploaded where they are read
+                table = self._upload([p + [-1] * (width - len(p)) for p in tables]).view(len(tables), width)
+                start = self._upload([s.len for s in seqs])
+                cu = None
+                if any(c != 1 for c in counts):
+                    cu = self._upload([0, *itertools.accumulate(counts)])
+                self.ops.write(self.kv, K, V, table, start, cu, stream)
+
+        self._own("append", seqs, counts, stream, write if shape[0] else None)
+        for seq, c in zip(seqs, counts):
+            seq.len += c
+
+    def reserve(self, sids, counts=None, stream=None):
+        """Pages for the next counts[i] tokens of sequence sids[i] (default one
+        each) that something else writes, a decode step for one: `table` names
+        them afterwards.  Tell with `advance` how many were written."""
+        seqs, counts = self._counts("reserve", sids, counts)
+        self._own("reserve", seqs, counts, stream)
+
+    def advance(self, sids, counts=None):
+        """Count tokens that were written into reserved pages."""
+        seqs, counts = self._counts("advance", sids, counts)
+        for sid, seq, c in zip(sids, seqs, counts):
+            if seq.len + c > len(seq.pages) * self.kv.page:
+                raise ValueError(f"advance: sequence {sid} has pages for {len(seq.pages) * self.kv.page} tokens, not {seq.len + c}")
+        for seq, c in zip(seqs, counts):
+            seq.len += c
 
     def compact(self, stream=None) -> int:
         """Move the used pages to the lowest numbers.  Returns how many moved;

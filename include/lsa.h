@@ -293,6 +293,37 @@ lsa_status lsa_select_attn(const uint16_t* Q, const uint16_t* K,
                            const lsa_cfg* cfg, uint16_t* O, void* ws,
                            size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------- paged 8-bit K/V cache */
+
+/*
+ * K/V of one layer in 8 bits, in pages that sequences own through a table
+ * [essay ch. 8: the method stacks with 8-bit quantisation; the pages give no
+ * layout].  Page p holds `page` consecutive tokens of one sequence:
+ *   K, V   [n_pages, hkv, page, d_head] codes: OCP e4m3 (fmt LSA_KV8_E4M3) or
+ *          two's complement int8 in -127 .. 127 (LSA_KV8_INT8);
+ *   scale  [n_pages, hkv, 2] fp32, K's and V's: powers of two 2^e with
+ *          -100 <= e <= 120.  A code's value is code * scale.
+ * Token t of sequence b is row t % page of page table[b, t / page]; `table`
+ * is int32 [n_seq, max_pages] on the device, entries behind a sequence's last
+ * page are not read.  Sequences may share pages (a forked prefix): reading
+ * them is always allowed, lsa_kv8_write must be given pages of its own.
+ * A page number outside the pool, or a token range outside the table, raises
+ * the device error word (LSA_EDEVICE at the next lsa_check_device_error) and
+ * the rows concerned are skipped.  page is 16, 32, 64, 128 or 256; n_pages *
+ * hkv * page < 2^31; K and V 128-byte aligned, scale 8-byte.
+ */
+#define LSA_KV8_E4M3 0
+#define LSA_KV8_INT8 1
+typedef struct lsa_kv8 {
+    int32_t  fmt;       /* LSA_KV8_E4M3 or LSA_KV8_INT8 */
+    int32_t  hkv;
+    int32_t  page;      /* tokens per page              */
+    int64_t  n_pages;
+    uint8_t* K;
+    uint8_t* V;
+    float*   scale;
+} lsa_kv8;
+
 /* ------------------------------------------------------------ decode */
 
 /*
@@ -320,6 +351,17 @@ lsa_status lsa_select_attn(const uint16_t* Q, const uint16_t* K,
  * at row r*(cap - shared_len) + (t - shared_len).  shared_len is a multiple
  * of 512 below cap, and lsa_decode_load needs n >= shared_len.  Each request
  * keeps its own cache (its blocks are clustered once per request).
+ *
+ * Paged 8-bit keys and values (optional; kv8 = NULL for none): request r's
+ * token t lives in page kv8_table[r, t / page] of *kv8 (see lsa_kv8 above)
+ * instead of the pools, lsa_decode_step writes it with lsa_kv8_write and
+ * attends with lsa_kv8_sparse_attn; what is selected stays the same.  The
+ * table must name a page for every token a request holds by the end of a call;
+ * requests may share the full pages of a common prefix, and shared_len must be
+ * 0.  K and V are then only what lsa_decode_load reads: the prompt's rows
+ * [n, hkv, d_head], whichever request it is; with V = NULL it takes the codes
+ * as written already.  lsa_decode_step reads neither.  q, k and v of a step
+ * must be 16-byte aligned.
  */
 typedef struct lsa_decode {
     int32_t   batch, hkv, hq;
@@ -333,6 +375,9 @@ typedef struct lsa_decode {
     const uint16_t* K_shared;
     const uint16_t* V_shared;
     int64_t   shared_len;
+    const lsa_kv8* kv8;        /* optional (NULL = none): keys and values in pages */
+    const int32_t* kv8_table;  /* device, [batch, kv8_max_pages]                   */
+    int32_t   kv8_max_pages;   /* kv8_max_pages * kv8->page >= cap                 */
 } lsa_decode;
 
 /* Workspace bytes of lsa_decode_load / lsa_decode_step for this state. */
@@ -588,36 +633,7 @@ lsa_status lsa_sparse_attn_partial(const uint16_t* Q, const uint16_t* K, const u
 lsa_status lsa_lse_combine(const float* O_parts, const float* lse_parts, int32_t world, int64_t nq,
                            int32_t hq, uint16_t* O, void* stream);
 
-/* ------------------------------------------------- paged 8-bit K/V cache */
-
-/*
- * K/V of one layer in 8 bits, in pages that sequences own through a table
- * [essay ch. 8: the method stacks with 8-bit quantisation; the pages give no
- * layout].  Page p holds `page` consecutive tokens of one sequence:
- *   K, V   [n_pages, hkv, page, d_head] codes: OCP e4m3 (fmt LSA_KV8_E4M3) or
- *          two's complement int8 in -127 .. 127 (LSA_KV8_INT8);
- *   scale  [n_pages, hkv, 2] fp32, K's and V's: powers of two 2^e with
- *          -100 <= e <= 120.  A code's value is code * scale.
- * Token t of sequence b is row t % page of page table[b, t / page]; `table`
- * is int32 [n_seq, max_pages] on the device, entries behind a sequence's last
- * page are not read.  Sequences may share pages (a forked prefix): reading
- * them is always allowed, lsa_kv8_write must be given pages of its own.
- * A page number outside the pool, or a token range outside the table, raises
- * the device error word (LSA_EDEVICE at the next lsa_check_device_error) and
- * the rows concerned are skipped.  page is 16, 32, 64, 128 or 256; n_pages *
- * hkv * page < 2^31; K and V 128-byte aligned, scale 8-byte.
- */
-#define LSA_KV8_E4M3 0
-#define LSA_KV8_INT8 1
-typedef struct lsa_kv8 {
-    int32_t  fmt;       /* LSA_KV8_E4M3 or LSA_KV8_INT8 */
-    int32_t  hkv;
-    int32_t  page;      /* tokens per page              */
-    int64_t  n_pages;
-    uint8_t* K;
-    uint8_t* V;
-    float*   scale;
-} lsa_kv8;
+/* ------------------------------------- paged 8-bit K/V cache: the calls */
 
 /*
  * lsa_kv8_write -- write new tokens' K/V rows into their pages.  K, V

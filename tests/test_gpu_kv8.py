@@ -571,3 +571,60 @@ def test_a_layer_over_the_cache(lsa, fmt):
     assert torch.equal(before[0], after[0]) and torch.equal(before[1], after[1])
     assert pages.used_pages == len(set(pages.pages(a)) | set(pages.pages(b))) == max(pages.pages(a) + pages.pages(b)) + 1
     lsa.check_device_error()
+
+
+@pytest.mark.parametrize("fmt,mode", [("e4m3", 0), ("int8", 1)])
+def test_decode_over_the_cache(lsa, fmt, mode):
+    """Decode steps with paged 8-bit keys and values select the same rows as
+    with bf16 pools, and attend over the codes."""
+    rng = np.random.default_rng(50)
+    batch, hkv, hq, cap, steps = 3, 2, 8, 2048, 6
+    cfg = lsa.Config(k=128, sinks=4, window=600, mode=mode)
+    W = torch.linalg.qr(torch.from_numpy(rng.standard_normal((128, 64))))[0].float().contiguous().cuda()
+    lens = [1021, 1534, 700]                     # two of them complete a block on the way
+    data = [[bf16(rng.standard_normal((n + steps, h, 128)))[0] for h in (hkv, hkv, hq)] for n in lens]
+    plain = lsa.Decode(batch, hkv, hq, cap, cfg)
+    dec = lsa.Decode(batch, hkv, hq, cap, cfg, kv8=fmt)
+    for r, (K, V, _) in enumerate(data):
+        for d in (plain, dec):
+            d.load(r, K[:lens[r]], V[:lens[r]], W)
+    assert dec.len == lens
+    for i in range(steps):
+        k, v, q = (torch.stack([data[r][j][lens[r] + i] for r in range(batch)]) for j in range(3))
+        rows = [torch.empty(batch, hkv, cfg.row, dtype=torch.int32, device="cuda") for _ in range(2)]
+        plain.step(q, k, v, W, W, idx_out=rows[0])
+        o = dec.step(q, k, v, W, W, idx_out=rows[1])
+        assert torch.equal(rows[0], rows[1])
+        now = [n + i + 1 for n in lens]
+        want = ref.lists(q.double().cpu().numpy(), *host(dec.kv8), dec.kv8_table.cpu().numpy(), now, [0, 1, 2],
+                         rows[1].cpu().numpy(), fmt)
+        close(o, want[0], want[2])
+    assert dec.len == now
+    lsa.check_device_error()
+
+
+def test_decode_requests_share_the_pages_of_a_prefix(lsa):
+    rng = np.random.default_rng(51)
+    hkv, hq, cap, n, steps = 2, 4, 1024, 700, 3
+    cfg = lsa.Config(k=64, sinks=4, window=512)
+    W = torch.linalg.qr(torch.from_numpy(rng.standard_normal((128, 64))))[0].float().contiguous().cuda()
+    K, V = (bf16(rng.standard_normal((n, hkv, 128)))[0] for _ in range(2))
+    pages = lsa.KV8Pages(lsa.KV8(30, hkv, page=64))
+    a = pages.add()
+    pages.append([a], K, V, [n])
+    ids = [a, pages.fork(a)]
+    table = torch.full((2, cap // 64), -1, dtype=torch.int32, device="cuda")
+    dec = lsa.Decode(2, hkv, hq, cap, cfg, kv8=pages.kv, kv8_table=table)
+    own = lsa.Decode(2, hkv, hq, cap, cfg, kv8="e4m3")
+    for r in range(2):
+        dec.load(r, K, V, W, written=True)
+        own.load(r, K, V, W)
+    for _ in range(steps):
+        q, k, v = (bf16(rng.standard_normal((2, h, 128)))[0] for h in (hq, hkv, hkv))
+        pages.reserve(ids)
+        table.copy_(pages.table(ids, width=table.shape[1])[0])
+        o = dec.step(q, k, v, W, W)
+        pages.advance(ids)
+        assert torch.equal(o, own.step(q, k, v, W, W))
+    assert pages.used_pages == 11 + 1            # eleven pages of the prompt, the open one twice
+    lsa.check_device_error()

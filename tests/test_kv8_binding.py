@@ -141,3 +141,39 @@ def test_abi_copy_refusals(L):
         assert b"lsa_kv8_copy_pages" in L.lsa_last_error()
     assert copy([0], [1], n=-1) == LSA_EINVAL and copy([0], [1], n=101) == LSA_EINVAL
     assert L.lsa_kv8_copy_pages(kv, None, None, 1, None) == LSA_EINVAL
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="passes fake device addresses: runs only where no GPU is present")
+def test_decode_refusals(L):
+    cfg = _lib.lsa_cfg()
+    L.lsa_cfg_default(ctypes.byref(cfg))
+    f = ctypes.c_void_p(0x10000)
+
+    def state(kv=(), **kw):
+        d = _lib.lsa_decode()
+        d.batch, d.hkv, d.hq, d.cap, d.U_blk = 2, 2, 8, 1024, 0x10000
+        c = d.cache
+        c.hkv, c.cap_units, c.cap_buckets = 4, 256, 128
+        for a in ("bucket_of_unit", "members", "offsets", "cnt_lr", "minlr", "maxpos", "sum", "cent", "units"):
+            setattr(c, a, 0x10000)
+        d.kv8 = ctypes.pointer(lsa_kv8(**{**dict(fmt=0, hkv=2, page=64, n_pages=64, K=0x10000, V=0x20000, scale=0x30000), **dict(kv)}))
+        d.kv8_table, d.kv8_max_pages = 0x10000, 16
+        for k, v in kw.items():
+            setattr(d, k, v)
+        return ctypes.byref(d)
+
+    def step(d, q=f, ws=f, nws=1 << 40):
+        return L.lsa_decode_step(d, q, f, f, f, f, ctypes.byref(cfg), f, None, ws, nws, None)
+
+    assert L.lsa_decode_workspace_bytes(ctypes.byref(cfg), state()) > 0
+    for d, want in ((state(kv8_max_pages=15), LSA_EINVAL), (state(kv8_table=None), LSA_EINVAL), (state(dict(hkv=4)), LSA_EINVAL),
+                    (state(dict(fmt=3)), LSA_EINVAL), (state(dict(page=40)), LSA_EUNSUPPORTED), (state(U_blk=None), LSA_EINVAL),
+                    (state(shared_len=512, K_shared=0x10000, V_shared=0x10000), LSA_EINVAL)):
+        assert step(d) == want
+        assert L.lsa_decode_workspace_bytes(ctypes.byref(cfg), d) == 0
+    assert step(state(), q=ctypes.c_void_p(0x10008)) == LSA_EINVAL
+    assert step(state(), ws=ctypes.c_void_p(0x10008)) == LSA_EINVAL
+    assert step(state(), nws=100) == LSA_ENOSPACE
+    load = lambda d, n=600: L.lsa_decode_load(d, 0, n, f, ctypes.byref(cfg), f, 1 << 40, None)  # noqa: E731
+    assert load(state()) == LSA_EINVAL and b"prompt" in L.lsa_last_error()
+    assert load(state(K=0x10008, V=0x10000)) == LSA_EINVAL

@@ -169,3 +169,35 @@ def test_refusals_change_nothing():
     p.append([], rows(rng, 0), rows(rng, 0))
     p.append([a], rows(rng, 0), rows(rng, 0), [0])
     assert state == (p.free_pages, p.pages(a), p.pages(b), list(p.refs))
+
+
+def test_reserve_and_advance():
+    rng = np.random.default_rng(6)
+    p = pool(8)
+    a = p.add()
+    p.append([a], rows(rng, 20), rows(rng, 20), [20])
+    b = p.fork(a)
+    before = content(p, a)
+    p.reserve([a, b], [13, 1])                                 # a third page for a, the open page copied for it
+    assert p.ops.copied == [1] and len(p.pages(a)) == 3 and len(p.pages(b)) == 2
+    assert p.pages(a)[0] == p.pages(b)[0] and p.pages(a)[1] != p.pages(b)[1]
+    assert p.len(a) == p.len(b) == 20
+    for s in (a, b):
+        for x, y in zip(content(p, s), before):
+            np.testing.assert_array_equal(x, y)
+    p.reserve([a, b], [13, 1])                                 # it has them
+    assert p.ops.copied == [1] and p.used_pages == 4
+    with pytest.raises(ValueError, match="pages for 32"):
+        p.advance([a, b], [5, 13])
+    assert p.len(a) == 20
+    p.advance([a], [13])
+    p.append([a], rows(rng, 15), rows(rng, 15), [15])          # fills the reserved page
+    assert p.len(a) == 48 and p.used_pages == 4
+    c = p.fork(a)
+    p.reserve([a], [20])
+    p.truncate(a, 40)                                          # gives the reserved pages back
+    assert len(p.pages(a)) == 3 and p.refs[p.pages(a)[2]] == 2
+    p.free(c)
+    with pytest.raises(LSAError):
+        p.reserve([a], [200])
+    assert len(p.pages(a)) == 3 and p.used_pages == 4
