@@ -718,7 +718,9 @@ def kv8_write(kv: KV8, K: torch.Tensor, V: torch.Tensor, table: torch.Tensor, st
     n = K.shape[0]
     if V.shape[0] != n:
         raise ValueError(f"V: expected shape {tuple(K.shape)}, got {tuple(V.shape)}")
-    pt = _arg(table, "table", I32, (None, None))
+    if table.dim() != 2:
+        _spec(table, "table", I32, (None, None))
+    pt = _arg(table, "table", I32, table.shape)
     n_seq, max_pages = table.shape
     ps = _arg(start, "start", I32, (n_seq,))
     pc = _arg(cu, "cu", I32, (n_seq + 1,))
@@ -742,15 +744,15 @@ def kv8_sparse_attn_workspace_bytes(kv: KV8, nq: int, hq: int, n_idx: int) -> in
     return int(lib().lsa_kv8_sparse_attn_workspace_bytes(kv._ref, nq, hq, n_idx))
 
 
-def _kv8_buffers(dev, nq, hq, O, lse, ws, need):
+def _kv8_buffers(dev, Q, O, lse, ws, need):
     """O, lse and ws, allocated where the caller gave none (or too small a ws),
     their addresses, and what was allocated."""
     made = []
     if O is None:
-        O = torch.empty((nq, hq, 128), dtype=BF16, device=dev)
+        O = torch.empty_like(Q, memory_format=torch.contiguous_format)
         made.append(O)
     if lse is None:
-        lse = torch.empty((nq, hq), dtype=F32, device=dev)
+        lse = Q.new_empty((Q.shape[0], Q.shape[1]), dtype=F32)
         made.append(lse)
     if ws is None or ws.numel() < need:
         ws = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
@@ -770,7 +772,9 @@ def kv8_attn(Q: torch.Tensor, kv: KV8, table: torch.Tensor, lens: torch.Tensor, 
     dev, L = kv.device, lib()
     pq, ld = _rows(Q, "Q", None)
     nq, hq, _ = Q.shape
-    pt = _arg(table, "table", I32, (None, None))
+    if table.dim() != 2:
+        _spec(table, "table", I32, (None, None))
+    pt = _arg(table, "table", I32, table.shape)
     n_seq, max_pages = table.shape
     pl = _arg(lens, "lens", I32, (n_seq,))
     pc = _arg(cu, "cu", I32, (n_seq + 1,))
@@ -780,7 +784,7 @@ def kv8_attn(Q: torch.Tensor, kv: KV8, table: torch.Tensor, lens: torch.Tensor, 
     if cu is None and nq != n_seq:
         raise ValueError(f"Q: without cu, expected one row for each of {n_seq} sequences, got {nq}")
     _on(dev, Q, table, lens, cu, O, lse, ws)
-    O, lse, po, pe, pw, nw, made = _kv8_buffers(dev, nq, hq, O, lse, ws,
+    O, lse, po, pe, pw, nw, made = _kv8_buffers(dev, Q, O, lse, ws,
                                                 L.lsa_kv8_attn_workspace_bytes(kv._ref, nq, hq, cu is None, n_seq, max_pages,
                                                                                sinks, window))
     _launch(kv, stream, "lsa_kv8_attn",
@@ -798,7 +802,9 @@ def kv8_sparse_attn(Q: torch.Tensor, kv: KV8, table: torch.Tensor, lens: torch.T
     dev, L = kv.device, lib()
     pq, ld = _rows(Q, "Q", None)
     nq, hq, _ = Q.shape
-    pt = _arg(table, "table", I32, (None, None))
+    if table.dim() != 2:
+        _spec(table, "table", I32, (None, None))
+    pt = _arg(table, "table", I32, table.shape)
     n_seq, max_pages = table.shape
     pl = _arg(lens, "lens", I32, (n_seq,))
     pi = _arg(idx, "idx", I32, (nq, kv.hkv, None))
@@ -810,7 +816,7 @@ def kv8_sparse_attn(Q: torch.Tensor, kv: KV8, table: torch.Tensor, lens: torch.T
         raise ValueError(f"Q: without seq, expected one row for each of {n_seq} sequences, got {nq}")
     _on(dev, Q, table, lens, idx, seq, O, lse, ws)
     n_idx = idx.shape[2]
-    O, lse, po, pe, pw, nw, made = _kv8_buffers(dev, nq, hq, O, lse, ws,
+    O, lse, po, pe, pw, nw, made = _kv8_buffers(dev, Q, O, lse, ws,
                                                 L.lsa_kv8_sparse_attn_workspace_bytes(kv._ref, nq, hq, n_idx))
     _launch(kv, stream, "lsa_kv8_sparse_attn",
             lambda s: L.lsa_kv8_sparse_attn(kv._ref, pq, ld, nq, hq, pb, pt, pl, n_seq, max_pages, pi, n_idx, po, pe,

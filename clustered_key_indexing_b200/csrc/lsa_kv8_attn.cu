@@ -29,6 +29,8 @@
 #include <float.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "lsa_common.cuh"
 #include "lsa_mma.cuh"
 
@@ -1030,12 +1032,23 @@ static int64_t kv8_max_chunks(int64_t nq, int32_t page, int32_t max_pages, int32
     return some < all ? some : all;
 }
 
+// A kernel's dynamic shared memory limit, raised once a device.
+static void kv8_allow_smem(const void* kern, size_t bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_acquire) & bit) return;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess)
+        done.fetch_or(bit, std::memory_order_release);
+}
+
 template <int FMT, int NT, bool LIST>
 static lsa_status launch_kv8_split(Kv8AttnArgs a, const Kv8Plan& p, int64_t n_seq, bool one_each, cudaStream_t st) {
     const int n = p.rows_per_seq > 0 ? (int)(p.rows_per_seq * n_seq) : kv8_ctas<NT>();
     a.rows_per_seq = (int32_t)p.rows_per_seq;
     const size_t smem = (size_t)kKv8Warps * kKv8Warp;
-    cudaFuncSetAttribute(kv8_split_kernel<FMT, NT, LIST>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<uint64_t> allowed{0};
+    kv8_allow_smem((const void*)kv8_split_kernel<FMT, NT, LIST>, smem, allowed);
     lsa_status s;
     {
         KTime kt_("kv8_split_kernel", st);
@@ -1162,7 +1175,8 @@ lsa_status lsa_kv8_sparse_attn(const lsa_kv8* kv, const uint16_t* Q, int64_t q_s
         const unsigned grid = (unsigned)ceil_div<int64_t>(nq * kv->hkv, kKv8ListWarps);
         auto kern = kv->fmt == LSA_KV8_E4M3 ? kv8_list_kernel<0> : kv8_list_kernel<1>;
         const int smem = kKv8ListWarps * kKv8Warp;
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        static std::atomic<uint64_t> allowed[2];
+        kv8_allow_smem((const void*)kern, smem, allowed[kv->fmt]);
         kern<<<grid, 32 * kKv8ListWarps, smem, st>>>(a);
     }
     return check_launch("kv8_list_kernel");
