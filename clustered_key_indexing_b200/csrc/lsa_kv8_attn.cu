@@ -52,7 +52,7 @@ struct Kv8AttnArgs {
     const int32_t* seq;    // lists: [nq] or NULL (query i is sequence i's)
     const int32_t* idx;    // lists: [nq, hkv, n_idx]
     int64_t q_stride, nq, n_pages;
-    int32_t n_seq, max_pages, hkv, G, lgp, n_idx;
+    int32_t n_seq, max_pages, hkv, G, lgG, lgp, n_idx;
     int32_t S, W;          // dense: sinks and window (W = 0: every key)
     uint16_t* O;           // [nq, hq, 128]
     float* lse;            // [nq, hq] or NULL
@@ -732,7 +732,11 @@ struct Kv8Scan {
                 total += all;
             }
         }
-        per = max((int64_t)least, (total + n_cta - 1) / n_cta);
+        // `least` a CTA, but no more than the rows have on average: short rows
+        // are not queued behind one another while CTAs are idle
+        const int64_t rows = (LIST ? a.nq : (int64_t)a.n_seq) * a.hkv;
+        const int64_t few = total < rows * least ? max((int64_t)1, (total + rows - 1) / rows) : least;
+        per = max(few, (total + n_cta - 1) / n_cta);
     }
     // The sequence whose chunks hold position w of the stream (0 <= w < total).
     __device__ __forceinline__ int64_t find(const Kv8AttnArgs& a, int64_t w, Kv8Seq& out) {
@@ -773,26 +777,29 @@ template <int NT>
 __device__ __forceinline__ int64_t kv8_out_row(const Kv8AttnArgs& a, const Kv8Seq& q, int cg, int g, int c) {
     const int64_t cc = (int64_t)cg * 8 * NT + c;
     if (cc >= (int64_t)q.n * a.G) return -1;
-    return (q.q0 + cc / a.G) * (a.G * a.hkv) + g * a.G + cc % a.G;
+    return (q.q0 + (cc >> a.lgG)) * (a.G * a.hkv) + g * a.G + (cc & (a.G - 1));
 }
 
-__device__ __forceinline__ void kv8_store(const Kv8AttnArgs& a, int64_t orow, int d, float acc, float m, float l) {
+// Four sums of one output row (dims d .. d + 3).
+__device__ __forceinline__ void kv8_store(const Kv8AttnArgs& a, int64_t orow, int d, float4 x, float m, float l) {
     const bool any = l > 0.f || l != l;
-    a.O[orow * kD + d] = bf16_bits(any ? acc / l : 0.f);
+    const float f = any ? 1.f / l : 0.f;
+    *reinterpret_cast<uint2*>(a.O + orow * kD + d) = make_uint2(pack_bf16x2(x.x * f, x.y * f), pack_bf16x2(x.z * f, x.w * f));
     if (d == 0 && a.lse) a.lse[orow] = any ? m - kKv8Head + log2f(l) : -CUDART_INF_F;
 }
 
-template <int FMT, int NT, bool LIST>
-__global__ void __launch_bounds__(32 * kKv8Warps, NT == 1 ? 2 : 1) kv8_split_kernel(Kv8AttnArgs a, int least) {
+// WARPS = 16 (twice the steps at a time, one CTA an SM): only a CTA a row.
+template <int FMT, int NT, bool LIST, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, NT == 1 && WARPS == 8 ? 2 : 1) kv8_split_kernel(Kv8AttnArgs a, int least) {
     extern __shared__ __align__(1024) uint8_t ksm[];
-    __shared__ float sml[kKv8Warps * 8 * NT * 2];                 // (m, l) of every warp's columns
+    __shared__ __align__(8) float sml[WARPS * 8 * NT * 2];                     // (m, l) of every warp's columns
     const uint32_t ring = smem_u32(ksm) + (threadIdx.x >> 5) * kKv8Warp;
     // a warp's sums go where its ring was: [8 NT][kKv8Pad] floats
     auto so = [&](int w) { return reinterpret_cast<float*>(ksm + w * kKv8Warp); };
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, gq = lane >> 2, tq = lane & 3;
     Kv8Seq q;
     int64_t b, w0, w1;
-    if (a.rows_per_seq > 0) {  // a CTA for each row
+    if (WARPS != kKv8Warps || a.rows_per_seq > 0) {  // a CTA for each row
         b = blockIdx.x / a.rows_per_seq;
         const int r = blockIdx.x % a.rows_per_seq;
         kv8_seq<NT, LIST>(a, b, q);
@@ -816,10 +823,11 @@ __global__ void __launch_bounds__(32 * kKv8Warps, NT == 1 ? 2 : 1) kv8_split_ker
             q.base = next;
         }
         const int64_t rel = w - q.base;
-        const int r = (int)(rel / q.chunks), t0 = (int)(rel % q.chunks);
+        const int r = rel >> 31 ? (int)(rel / q.chunks) : (int)((uint32_t)rel / (uint32_t)q.chunks);
+        const int t0 = (int)(rel - (int64_t)r * q.chunks);
         const int g = r / q.groups, cg = r % q.groups;
         const int n = (int)min((int64_t)(q.chunks - t0), w1 - w);
-        const int ta = t0 + (int)((int64_t)n * wid / kKv8Warps), tb = t0 + (int)((int64_t)n * (wid + 1) / kKv8Warps);
+        const int ta = t0 + (int)((int64_t)n * wid / WARPS), tb = t0 + (int)((int64_t)n * (wid + 1) / WARPS);
 
         if (ta < tb) {
             Kv8State<NT> s;
@@ -835,15 +843,15 @@ __global__ void __launch_bounds__(32 * kKv8Warps, NT == 1 ? 2 : 1) kv8_split_ker
                 keys.g = g;
                 keys.n_sink = q.n_sink;
                 keys.c_lo = q.c_lo;
-                keys.tmin = first + c0 / a.G;
-                keys.tmax = first + c1 / a.G;
+                keys.tmin = first + (c0 >> a.lgG);
+                keys.tmax = first + (c1 >> a.lgG);
                 keys.lo = a.W > 0 ? keys.tmin - a.W + 1 : 0;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         const int cc = c0 + 8 * nt + 2 * tq + c;
-                        tc[nt][c] = cc <= c1 ? first + cc / a.G : -1;
+                        tc[nt][c] = cc <= c1 ? first + (cc >> a.lgG) : -1;
                     }
             }
             Kv8Walk<LIST> walk;
@@ -853,7 +861,7 @@ __global__ void __launch_bounds__(32 * kKv8Warps, NT == 1 ? 2 : 1) kv8_split_ker
             for (int nt = 0; nt < NT; ++nt) {
                 const int64_t cc = (int64_t)cg * 8 * NT + 8 * nt + gq;
                 row[nt] = cc < (int64_t)q.n * a.G
-                              ? a.Q + (q.q0 + cc / a.G) * a.q_stride + (int64_t)(g * a.G + cc % a.G) * kD : nullptr;
+                              ? a.Q + (q.q0 + (cc >> a.lgG)) * a.q_stride + (g * a.G + (cc & (a.G - 1))) * kD : nullptr;
             }
             const uint16_t* const (&crow)[NT] = row;
             kv8_load_q<NT>(s, crow, a.scale_log2);
@@ -881,27 +889,28 @@ __global__ void __launch_bounds__(32 * kKv8Warps, NT == 1 ? 2 : 1) kv8_split_ker
         __syncthreads();
         const bool final_ = n == q.chunks;
         float* part = a.part + ((int64_t)blockIdx.x * 2 + (t0 == 0 ? 1 : 0)) * kv8_part_floats<NT>();
-        for (int e = tid; e < 8 * NT * kD; e += 32 * kKv8Warps) {
-            const int c = e / kD, dim = e % kD;
+        for (int e = tid; e < 8 * NT * kD / 4; e += 32 * WARPS) {  // four sums of a column
+            const int c = e / (kD / 4), dim = e % (kD / 4) * 4;
             const int64_t orow = kv8_out_row<NT>(a, q, cg, g, c);
             if (orow < 0) continue;
-            float M = -FLT_MAX, l = 0.f, acc = 0.f;
+            float M = -FLT_MAX, l = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int i = 0; i < kKv8Warps; ++i) M = fmaxf(M, sml[2 * (i * 8 * NT + c)]);
+            for (int i = 0; i < WARPS; ++i) M = fmaxf(M, sml[2 * (i * 8 * NT + c)]);
 #pragma unroll
-            for (int i = 0; i < kKv8Warps; ++i) {
-                const int col = i * 8 * NT + c;
-                const float li = sml[2 * col + 1];
-                if (li == -1.f) continue;
-                const float f = ex2(sml[2 * col] - M);
-                l += li * f;
-                acc += so(i)[c * kKv8Pad + dim] * f;
+            for (int i = 0; i < WARPS; ++i) {
+                const float2 ml = *reinterpret_cast<const float2*>(sml + 2 * (i * 8 * NT + c));
+                if (ml.y == -1.f) continue;
+                const float f = ex2(ml.x - M);
+                const float4 x = *reinterpret_cast<const float4*>(so(i) + c * kKv8Pad + dim);
+                l += ml.y * f;
+                acc = make_float4(acc.x + x.x * f, acc.y + x.y * f, acc.z + x.z * f, acc.w + x.w * f);
             }
             if (final_) {
                 kv8_store(a, orow, dim, acc, M, l);
             } else {
-                part[c * kD + dim] = acc;
-                if (dim == 0) { part[8 * NT * kD + 2 * c] = M; part[8 * NT * kD + 2 * c + 1] = l; }
+                *reinterpret_cast<float4*>(part + c * kD + dim) = acc;
+                if (dim == 0) *reinterpret_cast<float2*>(part + 8 * NT * kD + 2 * c) = make_float2(M, l);
             }
         }
         __syncthreads();
@@ -945,7 +954,8 @@ __global__ void __launch_bounds__(32 * kKv8Warps) kv8_join_kernel(Kv8AttnArgs a,
     if (w1 < scan.total) scan.find(a, w1, q);
     asm volatile("griddepcontrol.wait;\n" ::: "memory");  // before any exit: this grid's end is the call's end
     if (w1 >= scan.total) return;
-    const int r = (int)((w1 - q.base) / q.chunks);
+    const int64_t rel = w1 - q.base;
+    const int r = rel >> 31 ? (int)(rel / q.chunks) : (int)((uint32_t)rel / (uint32_t)q.chunks);
     const int64_t begin = q.base + (int64_t)r * q.chunks, end = begin + q.chunks;
     if (begin == w1 || begin < w0) return;
     const int n = (int)((end - 1) / scan.per - c) + 1;
@@ -956,10 +966,7 @@ __global__ void __launch_bounds__(32 * kKv8Warps) kv8_join_kernel(Kv8AttnArgs a,
             if (orow < 0) return;
             float M, l;
             const float4 x = kv8_join_column<NT>(a, c, col, 0, 1, n, M, l);
-            const bool any = l > 0.f || l != l;
-            const float f = any ? 1.f / l : 0.f;
-            reinterpret_cast<uint2*>(a.O + orow * kD)[lane] = make_uint2(pack_bf16x2(x.x * f, x.y * f), pack_bf16x2(x.z * f, x.w * f));
-            if (lane == 0 && a.lse) a.lse[orow] = any ? M - kKv8Head + log2f(l) : -CUDART_INF_F;
+            kv8_store(a, orow, 4 * lane, x, M, l);
         }
         return;
     }
@@ -971,19 +978,19 @@ __global__ void __launch_bounds__(32 * kKv8Warps) kv8_join_kernel(Kv8AttnArgs a,
     s_acc[wid][lane] = kv8_join_column<NT>(a, c, blockIdx.y, wid, kKv8Warps, n, M, l);
     if (lane == 0) s_ml[wid] = make_float2(M, l);
     __syncthreads();
-    if (threadIdx.x >= kD) return;
-    const int dim = threadIdx.x;
-#pragma unroll
-    for (int i = 0; i < kKv8Warps; ++i) M = i == 0 ? s_ml[0].x : fmaxf(M, s_ml[i].x);
-    float sum = 0.f;
+    if (wid > 0) return;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
     l = 0.f;
+#pragma unroll
+    for (int i = 0; i < kKv8Warps; ++i) M = fmaxf(M, s_ml[i].x);
 #pragma unroll
     for (int i = 0; i < kKv8Warps; ++i) {
         const float f = ex2(s_ml[i].x - M);
+        const float4 x = s_acc[i][lane];
         l += s_ml[i].y * f;
-        sum += reinterpret_cast<const float*>(s_acc[i])[dim] * f;
+        sum = make_float4(sum.x + x.x * f, sum.y + x.y * f, sum.z + x.z * f, sum.w + x.w * f);
     }
-    kv8_store(a, orow, dim, sum, M, l);
+    kv8_store(a, orow, 4 * lane, sum, M, l);
 }
 
 // ------------------------------------------------------------- host side
@@ -1042,19 +1049,30 @@ static void kv8_allow_smem(const void* kern, size_t bytes, std::atomic<uint64_t>
         done.fetch_or(bit, std::memory_order_release);
 }
 
-template <int FMT, int NT, bool LIST>
-static lsa_status launch_kv8_split(Kv8AttnArgs a, const Kv8Plan& p, int64_t n_seq, bool one_each, cudaStream_t st) {
-    const int n = p.rows_per_seq > 0 ? (int)(p.rows_per_seq * n_seq) : kv8_ctas<NT>();
-    a.rows_per_seq = (int32_t)p.rows_per_seq;
-    const size_t smem = (size_t)kKv8Warps * kKv8Warp;
+template <int FMT, int NT, bool LIST, int WARPS>
+static lsa_status launch_kv8_ctas(const Kv8AttnArgs& a, int n, cudaStream_t st) {
+    constexpr size_t smem = (size_t)WARPS * kKv8Warp;
     static std::atomic<uint64_t> allowed{0};
-    kv8_allow_smem((const void*)kv8_split_kernel<FMT, NT, LIST>, smem, allowed);
-    lsa_status s;
+    kv8_allow_smem((const void*)kv8_split_kernel<FMT, NT, LIST, WARPS>, smem, allowed);
     {
         KTime kt_("kv8_split_kernel", st);
-        kv8_split_kernel<FMT, NT, LIST><<<n, 32 * kKv8Warps, smem, st>>>(a, kKv8Least);
+        kv8_split_kernel<FMT, NT, LIST, WARPS><<<n, 32 * WARPS, smem, st>>>(a, kKv8Least);
     }
-    if ((s = check_launch("kv8_split_kernel")) != LSA_OK || p.rows_per_seq > 0) return s;
+    return check_launch("kv8_split_kernel");
+}
+
+template <int FMT, int NT, bool LIST>
+static lsa_status launch_kv8_split(Kv8AttnArgs a, const Kv8Plan& p, int64_t n_seq, bool one_each, cudaStream_t st) {
+    a.rows_per_seq = (int32_t)p.rows_per_seq;
+    if (p.rows_per_seq > 0) {
+        const int rows = (int)(p.rows_per_seq * n_seq);
+        if constexpr (NT == 1)
+            if (rows <= num_sms()) return launch_kv8_ctas<FMT, 1, LIST, 16>(a, rows, st);
+        return launch_kv8_ctas<FMT, NT, LIST, kKv8Warps>(a, rows, st);
+    }
+    const int n = kv8_ctas<NT>();
+    lsa_status s;
+    if ((s = launch_kv8_ctas<FMT, NT, LIST, kKv8Warps>(a, n, st)) != LSA_OK) return s;
     // the join's own scan runs while the split kernel drains
     cudaLaunchConfig_t cfg{};
     // a row's pieces: about n over the rows; rows of up to 16 by whole columns
@@ -1101,6 +1119,7 @@ static Kv8AttnArgs kv8_args(const lsa_kv8* kv, const uint16_t* Q, int64_t q_stri
     a.table = table; a.lens = lens; a.n_seq = n_seq; a.max_pages = max_pages; a.hkv = kv->hkv; a.G = hq / kv->hkv;
     a.n_pages = kv->n_pages;
     while ((1 << a.lgp) < kv->page) ++a.lgp;
+    while ((1 << a.lgG) < a.G) ++a.lgG;
     a.O = O; a.lse = lse; a.part = (float*)ws;
     a.scale_log2 = 1.4426950408889634f / sqrtf((float)kD);
     return a;
