@@ -995,10 +995,16 @@ __global__ void __launch_bounds__(32 * kKv8Warps) kv8_join_kernel(Kv8AttnArgs a,
 
 // ------------------------------------------------------------- host side
 
-// Chunks a CTA of the stream takes at least (one a warp), and chunks a row may
-// have for a CTA of its own (six a warp).
+// Chunks a CTA of the stream takes at least (one a warp).
 constexpr int kKv8Least = 8;
-constexpr int kKv8Own = 48;
+
+// Chunks a row may have for a CTA of its own.  A row's CTA takes 4.5 us and
+// 2.2 us for each chunk of its warps; the stream takes 10 us before it wins by
+// spreading few rows over the GPU, and two pieces a CTA when rows are many.
+// Measured (own CTA / stream, us): 8 rows of 32 chunks 9.3 / 10.2, of 48 11.3 /
+// 10.4; 64 rows of 94 chunks 18.1 / 19.2, of 128 22.3 / 20.4; 128 rows of 128
+// chunks 26 / 33, of ragged lengths up to that 22 / 26; 512 rows of 128 89 / 94.
+static int64_t kv8_own_chunks(int64_t rows) { return rows < 104 ? 24 + rows : 128; }
 
 template <int NT>
 static int kv8_ctas() { return num_sms() * (NT == 1 ? 2 : 1); }
@@ -1026,7 +1032,7 @@ static Kv8Plan kv8_plan(bool lists, int64_t nq, int64_t n_seq, int G, int32_t hk
     // one sequence can have all new tokens
     const int64_t rows = hkv * (lists || one_each ? 1 : ceil_div<int64_t>(nq * G, 8 * p.nt));
     // CTAs without a row exit at once, but not for free: at most four a CTA of the stream
-    if (max_chunks <= kKv8Own && rows * n_seq <= 4 * ctas) p.rows_per_seq = rows;
+    if (max_chunks <= kv8_own_chunks(rows * n_seq) && rows * n_seq <= 4 * ctas) p.rows_per_seq = rows;
     else p.ws = (size_t)ctas * 2 * (p.nt == 1 ? kv8_part_floats<1>() : kv8_part_floats<2>()) * sizeof(float);
     return p;
 }
