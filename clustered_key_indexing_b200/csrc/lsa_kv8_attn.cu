@@ -534,10 +534,10 @@ __device__ __forceinline__ void kv8_step(const Kv8AttnArgs& a, const Kv8Keys<LIS
     kv8_pv<FMT, NT>(s, v, pb);
 }
 
-// Chunks [c, cend) of a row into the warp's state.  Copies run two steps ahead
+// Chunks c, c + STEP, ... below cend of a row into the warp's state.  Copies run two steps ahead
 // of their use, table entries and scales a chunk further, list entries two.
 // start() brings the first chunk on its way, so that Q can be read meanwhile.
-template <bool LIST>
+template <bool LIST, int STEP>
 struct Kv8Walk {
     Kv8Copy cp;
     int c, cend;
@@ -549,8 +549,8 @@ struct Kv8Walk {
         cend = cend_;
         cp = kv8_copy(a, ring);
         const int p0 = r.entry(a, c, cend);
-        p1 = r.entry(a, c + 1, cend);
-        p2 = r.entry(a, c + 2, cend);
+        p1 = r.entry(a, c + STEP, cend);
+        p2 = r.entry(a, c + 2 * STEP, cend);
         const int pid0 = r.page(a, p0);
         pid1 = r.page(a, p1);
         int row = r.row(a, p0, pid0);
@@ -567,7 +567,7 @@ struct Kv8Walk {
         constexpr int kSlot = 2 * kKv8Step, kLast = (kKv8Stages - 1) * kSlot;
         int slot = 0;
         uint32_t note = cp.note, note1 = cp.note + kKv8Note;
-        for (; c < cend; ++c) {
+        for (; c < cend; c += STEP) {
             int row1 = r.row(a, p1, pid1);
             const unsigned valid1 = kv8_fill_rows(row1);
             const int key = LIST ? 0 : r.key0(c);
@@ -576,7 +576,7 @@ struct Kv8Walk {
             cp_async_wait<1>();
             __syncwarp();
             kv8_issue(cp, note1, slot == 0 ? kLast : slot - kSlot, 0, valid1 & 0xFFFFu);
-            const int pid2 = r.page(a, p2), p3 = r.entry(a, c + 3, cend);
+            const int pid2 = r.page(a, p2), p3 = r.entry(a, c + 3 * STEP, cend);
             if (valid & 0xFFFFu) kv8_step<FMT, NT, LIST>(a, r, s, cp.ring + slot, note, 0, valid & 0xFFFFu, tc, key);
             cp_async_wait<1>();
             __syncwarp();
@@ -610,7 +610,7 @@ __global__ void __launch_bounds__(32 * kKv8ListWarps, 2) kv8_list_kernel(Kv8Attn
     const Kv8Keys<true> r = kv8_list(a, q, g);
     extern __shared__ __align__(1024) uint8_t lsm[];
     const int tc[1][2] = {{0, 0}};
-    Kv8Walk<true> walk;
+    Kv8Walk<true, 1> walk;
     walk.start(a, r, 0, (a.n_idx + 31) / 32, smem_u32(lsm) + (threadIdx.x >> 5) * kKv8Warp);
     kv8_load_q<1>(s, row, a.scale_log2);
     walk.template run<FMT, 1>(a, r, tc, s);
@@ -827,7 +827,7 @@ __global__ void __launch_bounds__(32 * WARPS, NT == 1 && WARPS == 8 ? 2 : 1) kv8
         const int t0 = (int)(rel - (int64_t)r * q.chunks);
         const int g = r / q.groups, cg = r % q.groups;
         const int n = (int)min((int64_t)(q.chunks - t0), w1 - w);
-        const int ta = t0 + (int)((int64_t)n * wid / WARPS), tb = t0 + (int)((int64_t)n * (wid + 1) / WARPS);
+        const int ta = t0 + wid, tb = t0 + n;  // neighbouring chunks at the same time: whole pages of DRAM
 
         if (ta < tb) {
             Kv8State<NT> s;
@@ -854,7 +854,7 @@ __global__ void __launch_bounds__(32 * WARPS, NT == 1 && WARPS == 8 ? 2 : 1) kv8
                         tc[nt][c] = cc <= c1 ? first + (cc >> a.lgG) : -1;
                     }
             }
-            Kv8Walk<LIST> walk;
+            Kv8Walk<LIST, WARPS> walk;
             walk.start(a, keys, ta, tb, ring);
             const uint16_t* row[NT];
 #pragma unroll
