@@ -93,22 +93,30 @@ __device__ __forceinline__ void kv8_new_tokens(const Kv8WriteArgs& a, int b, int
     }
 }
 
-// One CTA per (page the call touches, kv-head), for K and V both where their
-// rows fit the registers (pages of up to 64 tokens; else blockIdx.y tells which):
-// the new rows are held (16 rows a pass, 16 lanes of 16 bytes a row) between
-// the pass that finds their largest magnitude and the one that writes their
-// codes, so HBM sees each input once and each code once.  The heads of a page
-// are neighbours in the grid: together they read whole token rows.  Every CTA
-// finds its page by a scan over the sequences' page counts.
+// One CTA per (page the call touches, group of kv-heads): K and V of as many
+// heads as fit 32 registers a thread (pages of 128 and 256 tokens: of one head
+// either K or V, blockIdx.y tells which).  The new rows are held (16 rows a
+// pass, 16 lanes of 16 bytes a row) between the pass that finds their largest
+// magnitude and the one that writes their codes, so HBM sees each input once
+// and each code once.  The heads of a page are neighbours in the grid: together
+// they read whole token rows.  Every CTA finds its page by a scan over the
+// sequences' page counts.  Bound by HBM: 128K tokens of 8 heads in 140 us with
+// five CTAs an SM, 162 with the four that the compiler's registers left.
+__host__ __device__ constexpr int kv8_write_heads(int passes) { return passes >= 4 ? 1 : 4 / passes; }
+
 template <int FMT, int PASSES>
-__global__ void __launch_bounds__(256) kv8_write_kernel(Kv8WriteArgs a) {
-    constexpr int page = 16 * PASSES, NKV = PASSES <= 4 ? 2 : 1;
+__global__ void __launch_bounds__(256, PASSES <= 8 ? 5 : 2) kv8_write_kernel(Kv8WriteArgs a) {
+    constexpr int page = 16 * PASSES, HEADS = kv8_write_heads(PASSES);
+    constexpr int NKV = PASSES <= 4 ? 2 : 1, N = HEADS * NKV;  // tensors of this CTA: head j / NKV's K and V in turn
     __shared__ int64_t s_at[4];       // first new row's position, one past the last, first row of the call, page index
     __shared__ int32_t s_seq;
-    __shared__ uint32_t s_max[NKV][8];
+    __shared__ uint32_t s_max[N][8];
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-    const int64_t item = blockIdx.x / a.hkv;
-    const int h = blockIdx.x % a.hkv;
+    const int groups = (a.hkv + HEADS - 1) / HEADS;
+    const int64_t item = blockIdx.x / groups;
+    const int h0 = (int)(blockIdx.x % groups) * HEADS;
+    auto head = [&](int j) { return h0 + j / NKV; };
+    auto is_v = [&](int j) { return NKV == 2 ? (j & 1) : (int)blockIdx.y; };
     if (wid == 0) {
         if (a.cu == nullptr) {  // one token per sequence (touched page b is sequence b's) or one sequence's first pages
             if (lane == 0) {
@@ -150,17 +158,16 @@ __global__ void __launch_bounds__(256) kv8_write_kernel(Kv8WriteArgs a) {
     const int r1 = (int)min((int64_t)page, p1 - pg * page);
     const int rr = tid >> 4, c = tid & 15;
 
-    uint4 x[NKV][PASSES];
+    uint4 x[N][PASSES];
 #pragma unroll
-    for (int j = 0; j < NKV; ++j) {
-        const bool v = NKV == 2 ? j == 1 : blockIdx.y == 1;
-        const int64_t stride = v ? a.v_stride : a.k_stride;
-        const uint16_t* src = (v ? a.V : a.K) + (s_at[2] + pg * page - p0) * stride + (int64_t)h * kD;  // row 0 of the page
+    for (int j = 0; j < N; ++j) {
+        const int64_t stride = is_v(j) ? a.v_stride : a.k_stride;
+        const uint16_t* src = (is_v(j) ? a.V : a.K) + (s_at[2] + pg * page - p0) * stride + (int64_t)head(j) * kD;  // row 0 of the page
 #pragma unroll
         for (int i = 0; i < PASSES; ++i) {
             const int r = 16 * i + rr;
             x[j][i] = make_uint4(0u, 0u, 0u, 0u);
-            if (r >= r0 && r < r1) x[j][i] = __ldcs(reinterpret_cast<const uint4*>(src + r * stride + c * 8));
+            if (r >= r0 && r < r1 && head(j) < a.hkv) x[j][i] = __ldg(reinterpret_cast<const uint4*>(src + r * stride + c * 8));
         }
     }
     const int64_t pid = a.table[(int64_t)seq * a.max_pages + pg];
@@ -168,11 +175,11 @@ __global__ void __launch_bounds__(256) kv8_write_kernel(Kv8WriteArgs a) {
         if (tid == 0) raise_device_error(kErrKv8Page);
         return;
     }
-    float* sp = a.scale + (pid * a.hkv + h) * 2;
-    float old[NKV];
+    float* sp = a.scale + pid * a.hkv * 2;
+    float old[N];
 #pragma unroll
-    for (int j = 0; j < NKV; ++j) {
-        old[j] = r0 > 0 ? sp[NKV == 2 ? j : blockIdx.y] : 0.f;
+    for (int j = 0; j < N; ++j) {
+        old[j] = r0 > 0 && head(j) < a.hkv ? sp[head(j) * 2 + is_v(j)] : 0.f;
         uint32_t mx = 0u;
 #pragma unroll
         for (int i = 0; i < PASSES; ++i) {
@@ -189,9 +196,9 @@ __global__ void __launch_bounds__(256) kv8_write_kernel(Kv8WriteArgs a) {
     }
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < NKV; ++j) {
-        const bool v = NKV == 2 ? j == 1 : blockIdx.y == 1;
-        uint8_t* dst = (v ? a.Vp : a.Kp) + (pid * a.hkv + h) * (int64_t)page * kD;
+    for (int j = 0; j < N; ++j) {
+        if (head(j) >= a.hkv) continue;
+        uint8_t* dst = (is_v(j) ? a.Vp : a.Kp) + (pid * a.hkv + head(j)) * (int64_t)page * kD;
         uint32_t mx = 0u;
 #pragma unroll
         for (int i = 0; i < 8; ++i) mx = max(mx, s_max[j][i]);
@@ -223,7 +230,7 @@ __global__ void __launch_bounds__(256) kv8_write_kernel(Kv8WriteArgs a) {
             *reinterpret_cast<uint2*>(dst + r * kD + c * 8) =
                 make_uint2(kv8_pack4<FMT>(y[0], y[1], y[2], y[3]), kv8_pack4<FMT>(y[4], y[5], y[6], y[7]));
         }
-        if (tid == 0) sp[v] = s;
+        if (tid == 0) sp[head(j) * 2 + is_v(j)] = s;
     }
 }
 
@@ -287,7 +294,8 @@ static void launch_kv8_write(const Kv8WriteArgs& a, int page, dim3 grid, cudaStr
 static lsa_status run_kv8_write(const lsa_kv8* kv, const Kv8WriteArgs& a, int64_t items, cudaStream_t st) {
     {
         KTime kt_("kv8_write_kernel", st);
-        const dim3 grid((unsigned)(items * kv->hkv), kv->page <= 64 ? 1 : 2);
+        const int heads = kv8_write_heads(kv->page / 16);
+        const dim3 grid((unsigned)(items * ceil_div(kv->hkv, heads)), kv->page <= 64 ? 1 : 2);
         if (kv->fmt == LSA_KV8_E4M3) launch_kv8_write<0>(a, kv->page, grid, st);
         else launch_kv8_write<1>(a, kv->page, grid, st);
     }
