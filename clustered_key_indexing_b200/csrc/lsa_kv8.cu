@@ -64,6 +64,31 @@ __device__ __forceinline__ void kv8_unpack4(uint32_t w, float (&x)[4]) {
     }
 }
 
+constexpr int kKv8Warps = 8;  // warps of a CTA
+
+// Sum of v over the CTA's threads before this one, and over all of them.
+__device__ __forceinline__ long long kv8_block_scan(long long v, long long& all) {
+    __shared__ long long wsum[kKv8Warps];
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    long long inc = v;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const long long up = __shfl_up_sync(0xffffffffu, inc, off);
+        if (lane >= off) inc += up;
+    }
+    if (lane == 31) wsum[wid] = inc;
+    __syncthreads();
+    long long before = inc - v;
+    all = 0;
+#pragma unroll
+    for (int i = 0; i < kKv8Warps; ++i) {
+        if (i < wid) before += wsum[i];
+        all += wsum[i];
+    }
+    __syncthreads();
+    return before;
+}
+
 struct Kv8WriteArgs {
     const uint16_t* K;       // new rows [n_tokens, hkv, 128], token rows k_stride / v_stride elements apart
     const uint16_t* V;
@@ -79,15 +104,16 @@ struct Kv8WriteArgs {
 };
 
 // New tokens of sequence b: rows [q0, q0 + n) of the call, at positions
-// [start, start + n).  A range that does not fit the call or the table is
-// reported and counts as empty.
-__device__ __forceinline__ void kv8_new_tokens(const Kv8WriteArgs& a, int b, int page, int64_t& q0, int64_t& n,
-                                               int64_t& s0) {
+// [s0, s0 + n).  A range that does not fit the call or the table (or 31 bits)
+// is reported and counts as empty.
+__device__ __forceinline__ void kv8_new_tokens(const Kv8WriteArgs& a, int b, int page, int& q0, int& n, int& s0) {
     q0 = a.cu ? a.cu[b] : b;
-    n = a.cu ? (int64_t)a.cu[b + 1] - q0 : a.start ? 1 : a.n_tokens;
+    const int64_t m = a.cu ? (int64_t)a.cu[b + 1] - q0 : a.start ? 1 : a.n_tokens;
     s0 = a.start ? a.start[b] : 0;
-    if (n == 0) return;
-    if (q0 < 0 || n < 0 || q0 + n > a.n_tokens || s0 < 0 || s0 + n > (int64_t)a.max_pages * page) {
+    n = (int)m;
+    if (m == 0) return;
+    const int64_t room = min((int64_t)a.max_pages * page, (int64_t)0x7FFFFFFF);
+    if (q0 < 0 || m < 0 || q0 + m > a.n_tokens || s0 < 0 || s0 + m > room) {
         raise_device_error(kErrKv8Range);
         n = 0;
     }
@@ -108,61 +134,66 @@ template <int FMT, int PASSES>
 __global__ void __launch_bounds__(256, PASSES <= 8 ? 5 : 2) kv8_write_kernel(Kv8WriteArgs a) {
     constexpr int page = 16 * PASSES, HEADS = kv8_write_heads(PASSES);
     constexpr int NKV = PASSES <= 4 ? 2 : 1, N = HEADS * NKV;  // tensors of this CTA: head j / NKV's K and V in turn
-    __shared__ int64_t s_at[4];       // first new row's position, one past the last, first row of the call, page index
-    __shared__ int32_t s_seq;
     __shared__ uint32_t s_max[N][8];
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const int groups = (a.hkv + HEADS - 1) / HEADS;
-    const int64_t item = blockIdx.x / groups;
+    const int item = (int)(blockIdx.x / groups);
     const int h0 = (int)(blockIdx.x % groups) * HEADS;
     auto head = [&](int j) { return h0 + j / NKV; };
     auto is_v = [&](int j) { return NKV == 2 ? (j & 1) : (int)blockIdx.y; };
-    if (wid == 0) {
-        if (a.cu == nullptr) {  // one token per sequence (touched page b is sequence b's) or one sequence's first pages
-            if (lane == 0) {
-                const int b = a.start ? (int)item : 0;
-                int64_t q0, n, s0;
-                kv8_new_tokens(a, b, page, q0, n, s0);
-                s_seq = n > 0 ? b : -1;
-                s_at[0] = s0; s_at[1] = s0 + n; s_at[2] = q0; s_at[3] = a.start ? s0 / page : item;
-            }
-        } else {
-            if (lane == 0) s_seq = -1;
-            __syncwarp();
-            int64_t base = 0;
-            for (int b0 = 0; b0 < a.n_seq && base <= item; b0 += 32) {
-                const int b = b0 + lane;
-                int64_t q0 = 0, n = 0, s0 = 0, m = 0;
-                if (b < a.n_seq) kv8_new_tokens(a, b, page, q0, n, s0);
-                if (n > 0) m = (s0 + n - 1) / page - s0 / page + 1;
-                int64_t inc = m;
+    // the page: sequence s_at[0]'s page s_at[1], which the new tokens from
+    // position s_at[4] on touch, s_at[3] of them, the first row s_at[2] of the call
+    __shared__ int s_at[5];
+    auto found = [&](int b, int pg, int q0, int n, int p0) { s_at[0] = b; s_at[1] = pg; s_at[2] = q0; s_at[3] = n; s_at[4] = p0; };
+    int q0 = 0, n = 0, p0 = 0;
+    auto pages = [&]() { return n > 0 ? (p0 + n - 1) / page - p0 / page + 1 : 0; };
+    if (tid == 0) s_at[0] = -1;
+    if (a.cu == nullptr) {  // one token per sequence (touched page b is sequence b's) or one sequence's first pages
+        if (tid == 0) {
+            const int b = a.start ? item : 0;
+            kv8_new_tokens(a, b, page, q0, n, p0);
+            if (n > 0) found(b, a.start ? p0 / page : item, q0, n, p0);
+        }
+    } else if (a.n_seq <= 32) {  // one warp, a sequence a lane
+        if (wid == 0) {
+            if (lane < a.n_seq) kv8_new_tokens(a, lane, page, q0, n, p0);
+            const int m = pages();
+            int inc = m;
 #pragma unroll
-                for (int off = 1; off < 32; off <<= 1) {
-                    const int64_t up = __shfl_up_sync(0xffffffffu, inc, off);
-                    if (lane >= off) inc += up;
-                }
-                const int64_t k = item - (base + inc - m);
-                if (k >= 0 && k < m) {
-                    s_seq = b;
-                    s_at[0] = s0; s_at[1] = s0 + n; s_at[2] = q0; s_at[3] = s0 / page + k;
-                }
-                base += __shfl_sync(0xffffffffu, inc, 31);
+            for (int off = 1; off < 32; off <<= 1) {
+                const int up = __shfl_up_sync(0xffffffffu, inc, off);
+                if (lane >= off) inc += up;
             }
+            const int k = item - (inc - m);
+            __syncwarp();
+            if (k >= 0 && k < m) found(lane, p0 / page + k, q0, n, p0);
+        }
+    } else {
+        long long base = 0;
+        for (int b0 = 0; b0 < a.n_seq && base <= item; b0 += 256) {  // uniform: every thread holds the same base
+            const int b = b0 + tid;
+            q0 = n = p0 = 0;
+            if (b < a.n_seq) kv8_new_tokens(a, b, page, q0, n, p0);
+            const int m = pages();
+            long long all;
+            const long long k = item - (base + kv8_block_scan(m, all));
+            if (k >= 0 && k < m) found(b, p0 / page + (int)k, q0, n, p0);
+            base += all;
         }
     }
     __syncthreads();
-    const int seq = s_seq;
+    const int seq = s_at[0], pg = s_at[1];
     if (seq < 0) return;
-    const int64_t p0 = s_at[0], p1 = s_at[1], pg = s_at[3];
-    const int r0 = (int)max((int64_t)0, p0 - pg * page);                   // rows below r0 were written before
-    const int r1 = (int)min((int64_t)page, p1 - pg * page);
+    const int first = pg * page - s_at[4];                   // the page's first row, counted from the first new token
+    const int r0 = max(0, -first);                           // rows below r0 were written before
+    const int r1 = (int)min((int64_t)page, (int64_t)s_at[3] - first);
     const int rr = tid >> 4, c = tid & 15;
 
     uint4 x[N][PASSES];
 #pragma unroll
     for (int j = 0; j < N; ++j) {
         const int64_t stride = is_v(j) ? a.v_stride : a.k_stride;
-        const uint16_t* src = (is_v(j) ? a.V : a.K) + (s_at[2] + pg * page - p0) * stride + (int64_t)head(j) * kD;  // row 0 of the page
+        const uint16_t* src = (is_v(j) ? a.V : a.K) + ((int64_t)s_at[2] + first) * stride + (int64_t)head(j) * kD;  // row 0 of the page
 #pragma unroll
         for (int i = 0; i < PASSES; ++i) {
             const int r = 16 * i + rr;

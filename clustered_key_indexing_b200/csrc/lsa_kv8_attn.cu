@@ -36,7 +36,6 @@
 
 namespace lsa {
 
-constexpr int kKv8Warps = 8;
 constexpr int kKv8ListWarps = 8;
 constexpr float kKv8Head = 12.f;   // log2 of P's headroom
 constexpr float kKv8Lazy = 2.f;    // log2 growth that moves the running maximum
@@ -108,7 +107,7 @@ __device__ __forceinline__ uint32_t word_of(const uint4& v, int j) { return j ==
 template <int NT>
 struct Kv8State {
     uint32_t qb[NT][8][2];  // Q as B operands
-    float cf[NT][2];        // score factor of columns 2t, 2t + 1: Q's power of two * log2(e) / sqrt(d)
+    float cf[NT][2];        // Q's power of two of columns 2t, 2t + 1
     float o[NT][8][4];
     float m[NT][2], l[NT][2];
     float vref;             // the V scale that O is relative to
@@ -117,7 +116,7 @@ struct Kv8State {
 // Q row of each column (gq within tile nt; NULL: none), dims 32 t .. + 31 on
 // this lane, divided by the row's power of two.
 template <int NT>
-__device__ __forceinline__ void kv8_load_q(Kv8State<NT>& s, const uint16_t* const (&row)[NT], float scale_log2) {
+__device__ __forceinline__ void kv8_load_q(Kv8State<NT>& s, const uint16_t* const (&row)[NT]) {
     const int lane = threadIdx.x & 31, tq = lane & 3;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -137,8 +136,8 @@ __device__ __forceinline__ void kv8_load_q(Kv8State<NT>& s, const uint16_t* cons
         mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
         // |q| < 2^(E - 126): below 1 after the division by 2^e
-        const int e = mx == 0u ? 0 : max(-100, min(110, (int)(mx >> 7) - 126));
-        const float inv = __uint_as_float((uint32_t)(127 - e) << 23), f = __uint_as_float((uint32_t)(127 + e) << 23) * scale_log2;
+        const int e = mx == 0u ? 0 : max(-126, min(126, (int)(mx >> 7) - 126));
+        const float inv = __uint_as_float((uint32_t)(127 - e) << 23), f = __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
         for (int i = 0; i < 8; ++i)  // dims 32 t + 4 i .. + 3
 #pragma unroll
@@ -337,6 +336,8 @@ __device__ __forceinline__ Kv8Keys<true> kv8_list(const Kv8AttnArgs& a, int64_t 
     return r;
 }
 
+// The scales of a row; K's brings the scores to base 2 when it is noted (not
+// Q's factor: with a small Q that would be subnormal).
 __device__ __forceinline__ float2 kv8_scales(const Kv8AttnArgs& a, int row) {
     return __ldg(reinterpret_cast<const float2*>(a.scale) + (row >> a.lgp));
 }
@@ -401,8 +402,9 @@ __device__ __forceinline__ void kv8_note_rows(uint32_t note, int row) {
     asm volatile("st.shared.b32 [%0], %1;\n" ::"r"(note + 256 + 4 * ((e & 16) + 4 * (e & 3) + ((e >> 2) & 3))), "r"(row) : "memory");
 }
 
-__device__ __forceinline__ void kv8_note_scales(uint32_t note, float2 sc) {
-    asm volatile("st.shared.v2.f32 [%0], {%1, %2};\n" ::"r"(note + 8 * (threadIdx.x & 31)), "f"(sc.x), "f"(sc.y) : "memory");
+__device__ __forceinline__ void kv8_note_scales(const Kv8AttnArgs& a, uint32_t note, float2 sc) {
+    asm volatile("st.shared.v2.f32 [%0], {%1, %2};\n" ::"r"(note + 8 * (threadIdx.x & 31)), "f"(sc.x * a.scale_log2), "f"(sc.y)
+                 : "memory");
 }
 
 __device__ __forceinline__ float2 kv8_scale_of(uint32_t note, int e) {
@@ -559,7 +561,7 @@ struct Kv8Walk {
         __syncwarp();
         kv8_issue(cp, cp.note, 0, 0, valid & 0xFFFFu);
         kv8_issue(cp, cp.note, 2 * kKv8Step, 1, valid >> 16);
-        kv8_note_scales(cp.note, kv8_scales(a, row));
+        kv8_note_scales(a, cp.note, kv8_scales(a, row));
     }
 
     template <int FMT, int NT>
@@ -584,7 +586,7 @@ struct Kv8Walk {
             slot = slot == kLast ? 0 : slot + kSlot;
             if (valid >> 16) kv8_step<FMT, NT, LIST>(a, r, s, cp.ring + slot, note, 1, valid >> 16, tc, key + 16);
             slot = slot == kLast ? 0 : slot + kSlot;
-            kv8_note_scales(note1, sc1);
+            kv8_note_scales(a, note1, sc1);
             const uint32_t other = note;
             note = note1;
             note1 = other;
@@ -612,7 +614,7 @@ __global__ void __launch_bounds__(32 * kKv8ListWarps, 2) kv8_list_kernel(Kv8Attn
     const int tc[1][2] = {{0, 0}};
     Kv8Walk<true, 1> walk;
     walk.start(a, r, 0, (a.n_idx + 31) / 32, smem_u32(lsm) + (threadIdx.x >> 5) * kKv8Warp);
-    kv8_load_q<1>(s, row, a.scale_log2);
+    kv8_load_q<1>(s, row);
     walk.template run<FMT, 1>(a, r, tc, s);
     kv8_reduce_l<1>(s);
     // through shared memory (the ring's), [8][128] bf16, to whole lines
@@ -681,29 +683,6 @@ __device__ __forceinline__ void kv8_seq(const Kv8AttnArgs& a, int64_t b, Kv8Seq&
         q.n_sink = min((min(a.S, (int)len) + 31) / 32, q.c_lo);
         q.chunks = max(1, q.n_sink + hi - q.c_lo);
     }
-}
-
-// Sum of v over the CTA's threads before this one, and over all of them.
-__device__ __forceinline__ long long kv8_block_scan(long long v, long long& all) {
-    __shared__ long long wsum[kKv8Warps];
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    long long inc = v;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const long long up = __shfl_up_sync(0xffffffffu, inc, off);
-        if (lane >= off) inc += up;
-    }
-    if (lane == 31) wsum[wid] = inc;
-    __syncthreads();
-    long long before = inc - v;
-    all = 0;
-#pragma unroll
-    for (int i = 0; i < kKv8Warps; ++i) {
-        if (i < wid) before += wsum[i];
-        all += wsum[i];
-    }
-    __syncthreads();
-    return before;
 }
 
 template <int NT, bool LIST>
@@ -864,7 +843,7 @@ __global__ void __launch_bounds__(32 * WARPS, NT == 1 && WARPS == 8 ? 2 : 1) kv8
                               ? a.Q + (q.q0 + (cc >> a.lgG)) * a.q_stride + (g * a.G + (cc & (a.G - 1))) * kD : nullptr;
             }
             const uint16_t* const (&crow)[NT] = row;
-            kv8_load_q<NT>(s, crow, a.scale_log2);
+            kv8_load_q<NT>(s, crow);
             walk.template run<FMT, NT>(a, keys, tc, s);
             kv8_reduce_l<NT>(s);
 #pragma unroll
@@ -1026,8 +1005,11 @@ static Kv8Plan kv8_plan(bool lists, int64_t nq, int64_t n_seq, int G, int32_t hk
     Kv8Plan p{};
     p.nt = lists ? 1 : kv8_nt(nq, n_seq, G);
     const int ctas = p.nt == 1 ? kv8_ctas<1>() : kv8_ctas<2>();
-    // lists: rows that fill the GPU twice with a warp each
-    p.warps = lists && nq * hkv >= (int64_t)ctas * kKv8Warps * 2;
+    // lists: a warp a row from 1184 rows on (half the warps that fit), of short
+    // lists from 592 on.  Measured (warp / CTA a row, us): 97 chunks, 1024 rows
+    // 105 / 104, 2368 rows 169 / 218, 8000 rows 563 / 712; 25 chunks, 512 rows
+    // 30 / 23, 1024 rows 33 / 42; 7 chunks, 512 rows 12 / 13
+    p.warps = lists && (nq * hkv >= 4 * ctas || (nq * hkv >= 2 * ctas && max_chunks <= 32));
     if (p.warps) return p;
     // one sequence can have all new tokens
     const int64_t rows = hkv * (lists || one_each ? 1 : ceil_div<int64_t>(nq * G, 8 * p.nt));

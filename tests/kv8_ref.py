@@ -92,7 +92,7 @@ def attend(q, k, v, vtop):
     l = p.sum(1, keepdims=True)
     o, A = p @ v / l, p @ np.abs(v) / l
     d = 2.0 ** -23 * 136 * S + (n / 16 + 16) * 2.0 ** -23
-    tol = 2.0 ** -8 * np.abs(o) + (2.0 ** -11 + 2 * np.expm1(2 * d))[:, None] * A + n * 2.0 ** -37 * vtop / l
+    tol = 2.0 ** -8 * np.abs(o) + (2.0 ** -11 + 2 * np.expm1(np.minimum(2 * d, 50.0)))[:, None] * A + n * 2.0 ** -37 * vtop / l
     lse = (m[:, 0] + np.log(l[:, 0])) / np.log(2.0)
     return o, lse, tol, d / np.log(2.0) + np.abs(lse) * 2.0 ** -22 + 1e-6
 

@@ -108,6 +108,22 @@ def test_write_equals_the_formula(lsa, fmt, page, hkv, new, old):
     lsa.check_device_error()
 
 
+def test_write_many_sequences(lsa):
+    rng = np.random.default_rng(77)
+    n_seq, hkv, page = 700, 1, 16
+    old, new = rng.integers(0, 20, n_seq), rng.integers(0, 3, n_seq) * rng.integers(0, 12, n_seq)
+    table, n_pages = scattered(rng, (old + new).tolist(), page)
+    kv = random_cache(lsa, rng, n_pages, hkv, page, "int8")
+    K, V, scale = host(kv)
+    cu = np.concatenate([[0], np.cumsum(new)])
+    (k, hk), (v, hv) = (bf16(rng.standard_normal((cu[-1], hkv, 128)) * np.exp2(rng.integers(-3, 4, (cu[-1], 1, 1)))) for _ in range(2))
+    lsa.kv8_write(kv, k, v, i32(table), i32(old), cu=i32(cu))
+    ref.write(K, V, scale, hk, hv, table, old.tolist(), cu, "int8")
+    for g, w in zip(host(kv), (K, V, scale)):
+        np.testing.assert_array_equal(g, w)
+    lsa.check_device_error()
+
+
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 def test_write_token_by_token_grows_the_open_page(lsa, fmt):
     rng = np.random.default_rng(5)
@@ -219,7 +235,10 @@ def random_lists(rng, nq, hkv, n_idx, lens, seq, pads=0.2):
     (128, 2, 2, [40, 900], 50, 16),
     (16, 8, 4, [5000], 1, 2500),
     (256, 3, 4, [300, 1], 5, 0),
-    (64, 4, 2, [700, 600], 1300, 40),          # enough rows for one warp each
+    (64, 4, 2, [700, 600], 300, 1100),         # a warp a row, long lists
+    (64, 4, 2, [700, 600], 160, 40),           # a warp a row, short lists
+    (32, 8, 1, [700, 600], 100, 200),          # a CTA a row, more rows than SMs
+    (16, 2, 8, [900, 600], 60, 4200),          # pieces of rows
 ])
 def test_lists_against_64_bits(lsa, fmt, page, hkv, G, lens, nq, n_idx):
     rng = np.random.default_rng(nq + n_idx)
@@ -260,6 +279,28 @@ def test_scales_far_apart(lsa, fmt):
     close(lse, wl, tl)
     idx = np.tile(rng.permutation(n).astype(np.int32), (1, 1, 1))
     o, lse = lsa.kv8_sparse_attn(q, kv, i32(table), i32([n]), torch.from_numpy(idx).cuda())
+    close(o, wo, to)
+    close(lse, wl, tl)
+
+
+@pytest.mark.parametrize("e", [-120, 126])
+def test_queries_at_the_ends_of_the_range(lsa, e):
+    """Elements near bf16's largest and smallest magnitudes: no overflow on the
+    way to fp16 (against keys that bring the scores back to ordinary size)."""
+    rng = np.random.default_rng(12)
+    n = 40
+    kv = lsa.KV8(2, 1, page=32)
+    k, v = (bf16(rng.standard_normal((n, 1, 128)) * s)[0] for s in (2.0 ** max(-80, -e), 1.0))
+    lsa.kv8_write(kv, k, v, i32([[0, 1]]), i32([0]), cu=i32([0, n]))
+    q, hq = bf16(np.clip(rng.standard_normal((1, 2, 128)) * 0.9, -1.9, 1.9) * 2.0 ** e)
+    if e > 100:                                  # scores of 2^40 would be one key's: only one element of each query is large
+        q[..., 1:] = 0.0
+        hq[..., 1:] = 0.0
+        q[..., 0] = hq[..., 0] = 1.5 * 2.0 ** 126
+        kv.K.view(torch.uint8)[:, :, :, 0] = 0x38      # 1.0
+    o, lse = lsa.kv8_attn(q, kv, i32([[0, 1]]), i32([n]))
+    K, V, scale = host(kv)
+    wo, wl, to, tl = ref.attn(hq, K, V, scale, np.array([[0, 1]]), [n], [0, 1], "e4m3")
     close(o, wo, to)
     close(lse, wl, tl)
 
