@@ -421,8 +421,7 @@ class Decode:
                 raise ValueError("kv8_table: a cache of the caller's needs one")
             if kv8.hkv != hkv:
                 raise ValueError(f"kv8: expected {hkv} kv-heads, got {kv8.hkv}")
-            _arg(kv8_table, "kv8_table", I32, (batch, None))
-            _on(kv8.device, kv8_table)
+            _arg(kv8_table, "kv8_table", I32, (batch, None), kv8.index)
             if kv8_table.shape[1] * kv8.page < cap:
                 raise ValueError(f"kv8_table: {kv8_table.shape[1]} pages of {kv8.page} do not hold {cap} tokens")
         self.kv8, self.kv8_table = kv8, kv8_table
@@ -471,7 +470,8 @@ class Decode:
             self.V[r, :n].copy_(V)
         else:
             _need_cuda(K, V)
-            _on(self.kv8.device, K, V, W_k)
+            for name, x in (("K", K), ("V", V), ("W_k", W_k)):
+                _arg(x, name, x.dtype, x.shape, self.kv8.index)
             self.d.K, self.d.V = K.data_ptr() or None, None if written else V.data_ptr() or None
         check(lib().lsa_decode_load(ctypes.byref(self.d), r, self.shared_len + n, _ptr(W_k),
                                     ctypes.byref(self.cfg.c()), _ptr(self.ws), self.ws.numel(), _stream(stream)),
@@ -623,17 +623,17 @@ class KV8:
     @classmethod
     def of(cls, K: torch.Tensor, V: torch.Tensor, scale: torch.Tensor) -> "KV8":
         """A cache over arrays the caller holds."""
-        if K.dtype not in KV8_FMT:
-            raise TypeError(f"K: expected one of {tuple(KV8_FMT)}, got {K.dtype}")
-        if K.dim() != 4 or K.shape[3] != 128:
-            raise ValueError(f"K: expected shape ('*', '*', '*', 128), got {tuple(K.shape)}")
-        n_pages, hkv, page, _ = K.shape
-        _spec(V, "V", K.dtype, K.shape)
-        _spec(scale, "scale", F32, (n_pages, hkv, 2))
-        if page not in KV8_PAGES:
-            raise ValueError(f"page: expected one of {KV8_PAGES}, got {page}")
-        _need_cuda(K, V, scale)
-        _on(K.device, V, scale)
+        dtype, shape, dev = K.dtype, K.shape, K.get_device()
+        if dtype not in KV8_FMT:
+            raise TypeError(f"K: expected one of {tuple(KV8_FMT)}, got {dtype}")
+        if len(shape) != 4 or shape[3] != 128:
+            raise ValueError(f"K: expected shape ('*', '*', '*', 128), got {tuple(shape)}")
+        if shape[2] not in KV8_PAGES:
+            raise ValueError(f"page: expected one of {KV8_PAGES}, got {shape[2]}")
+        _arg(K, "K", dtype, shape, dev)
+        _arg(V, "V", dtype, shape, dev)
+        _arg(scale, "scale", F32, (shape[0], shape[1], 2), dev)
+        _on_gpu(dev)
         kv = cls.__new__(cls)
         kv._wrap(K, V, scale)
         return kv
@@ -643,69 +643,63 @@ class KV8:
         self.n_pages, self.hkv, self.page, _ = K.shape
         code = KV8_FMT[K.dtype]
         self.fmt = "int8" if code else "e4m3"
-        self.device = K.device
+        self.device, self.index = K.device, K.get_device()
         self.c = _lib.lsa_kv8(code, self.hkv, self.page, self.n_pages, K.data_ptr(), V.data_ptr(), scale.data_ptr())
         self._ref = ctypes.byref(self.c)
 
 
-def _on(dev, *ts):
-    """Every tensor lies on `dev`, a CUDA device."""
-    for t in ts:
-        if t is not None and t.device != dev:
-            if not t.is_cuda:
-                break
-            raise ValueError(f"LSA calls take tensors of one device: got {t.device} beside {dev}")
-    else:
-        if dev.type == "cuda":
-            return
-    raise ValueError("LSA calls take CUDA tensors (there is no CPU implementation)")
+# The calls below serve single decoded tokens, where a call's time is what the
+# host spends on it: each argument is looked at once, by its cheapest test.
+
+def _on_gpu(dev: int):
+    if dev < 0:
+        raise ValueError("LSA calls take CUDA tensors (there is no CPU implementation)")
 
 
-def _arg(t, name, dtype, shape):
-    """An argument's dtype, shape (None entries match any size) and layout.
-    Returns its address (None for None)."""
+def _arg(t, name, dtype, shape, dev: int):
+    """An argument's dtype, shape (None entries match any size), layout and
+    device number.  Returns its address (None for None)."""
     if t is None:
         return None
-    _spec(t, name, dtype, shape)
+    if t.dtype != dtype or t.shape != shape:
+        _spec(t, name, dtype, shape)
+    if t.get_device() != dev:
+        _on_gpu(t.get_device())
+        raise ValueError(f"LSA calls take tensors of one device: got {name} on {t.device} beside device {dev}")
     if not t.is_contiguous():
         raise ValueError("LSA calls take contiguous tensors")
     return t.data_ptr()
 
 
-def _rows(t, name, heads):
+def _rows(t, name, heads, dev: int):
     """A bf16 [n, heads, 128] tensor whose token rows are dense (their stride
-    may be larger: a slice of a fused projection).  Returns its address and the
-    elements between rows."""
-    if t.dtype != BF16 or t.dim() != 3 or t.shape[2] != 128 or (heads is not None and t.shape[1] != heads):
+    may be larger: a slice of a fused projection).  Returns its address, the
+    elements between rows, n and its heads."""
+    shape = t.shape
+    if t.dtype != BF16 or len(shape) != 3 or shape[2] != 128 or (heads is not None and shape[1] != heads):
         _spec(t, name, BF16, (None, heads, 128))
-    n, h, _ = t.shape
-    dense = h * 128
-    if t.is_contiguous():
-        return t.data_ptr(), dense
-    ld, sh, sd = t.stride()
-    if n <= 1:
-        ld = dense
-    if sd != 1 or (h > 1 and sh != 128) or ld < dense or ld % 8:
-        raise ValueError(f"{name}: token rows must be dense and a multiple of 8 elements apart, got strides {t.stride()}")
-    return t.data_ptr(), ld
+    n, h, _ = shape
+    ld = h * 128
+    if t.get_device() != dev:
+        _on_gpu(t.get_device())
+        raise ValueError(f"LSA calls take tensors of one device: got {name} on {t.device} beside device {dev}")
+    if not t.is_contiguous():
+        st, sh, sd = t.stride()
+        if sd != 1 or (h > 1 and sh != 128) or (n > 1 and (st < ld or st % 8)):
+            raise ValueError(f"{name}: token rows must be dense and a multiple of 8 elements apart, got strides {t.stride()}")
+        if n > 1:
+            ld = st
+    return t.data_ptr(), ld, n, h
 
 
-def _launch(kv, stream, name, call, *made):
-    """Run `call(stream handle)` with the cache's device current.  What the
-    call allocated (`made`) is kept from reuse until `stream` is done with it."""
-    dev = kv.device
-    if torch.cuda.current_device() != dev.index:
+def _launch(kv, stream, call, *args):
+    """call(*args, stream handle) with the cache's device current; its status."""
+    dev = kv.index
+    _on_gpu(dev)
+    if torch.cuda.current_device() != dev:
         with torch.cuda.device(dev):
-            return _launch(kv, stream, name, call, *made)
-    if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(dev.index)
-    else:
-        handle = stream.cuda_stream
-        for t in made:
-            t.record_stream(stream)
-    status = call(handle)
-    if status:
-        check(status, name)
+            return _launch(kv, stream, call, *args)
+    return call(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
 
 
 def kv8_write(kv: KV8, K: torch.Tensor, V: torch.Tensor, table: torch.Tensor, start: torch.Tensor, cu=None,
@@ -713,22 +707,21 @@ def kv8_write(kv: KV8, K: torch.Tensor, V: torch.Tensor, table: torch.Tensor, st
     """lsa_kv8_write: new tokens' K/V rows [n, hkv, 128] bf16 into the pages of
     their sequences: sequence b's rows cu[b] .. cu[b + 1] - 1 (cu None: one
     token each) at positions start[b] on, in pages table[b]."""
-    pk, ldk = _rows(K, "K", kv.hkv)
-    pv, ldv = _rows(V, "V", kv.hkv)
-    n = K.shape[0]
-    if V.shape[0] != n:
+    dev = kv.index
+    pk, ldk, n, _ = _rows(K, "K", kv.hkv, dev)
+    pv, ldv, nv, _ = _rows(V, "V", kv.hkv, dev)
+    if nv != n:
         raise ValueError(f"V: expected shape {tuple(K.shape)}, got {tuple(V.shape)}")
-    if table.dim() != 2:
-        _spec(table, "table", I32, (None, None))
-    pt = _arg(table, "table", I32, table.shape)
-    n_seq, max_pages = table.shape
-    ps = _arg(start, "start", I32, (n_seq,))
-    pc = _arg(cu, "cu", I32, (n_seq + 1,))
+    shape = table.shape
+    pt = _arg(table, "table", I32, shape if len(shape) == 2 else (None, None), dev)
+    n_seq, max_pages = shape
+    ps = _arg(start, "start", I32, (n_seq,), dev)
+    pc = _arg(cu, "cu", I32, (n_seq + 1,), dev)
     if cu is None and n != n_seq:
         raise ValueError(f"K: without cu, expected one row for each of {n_seq} sequences, got {n}")
-    _on(kv.device, K, V, table, start, cu)
-    _launch(kv, stream, "lsa_kv8_write",
-            lambda s: lib().lsa_kv8_write(kv._ref, pk, ldk, pv, ldv, n, pc, ps, pt, n_seq, max_pages, s))
+    status = _launch(kv, stream, lib().lsa_kv8_write, kv._ref, pk, ldk, pv, ldv, n, pc, ps, pt, n_seq, max_pages)
+    if status:
+        check(status, "lsa_kv8_write")
     return kv
 
 
@@ -744,22 +737,34 @@ def kv8_sparse_attn_workspace_bytes(kv: KV8, nq: int, hq: int, n_idx: int) -> in
     return int(lib().lsa_kv8_sparse_attn_workspace_bytes(kv._ref, nq, hq, n_idx))
 
 
-def _kv8_buffers(dev, Q, O, lse, ws, need):
-    """O, lse and ws, allocated where the caller gave none (or too small a ws),
-    their addresses, and what was allocated."""
-    made = []
+def _kv8_attend(kv, name, call, args, need, Q, n, h, O, lse, ws, stream):
+    """The tail of both attention calls: outputs and workspace that the caller
+    gave or that are made here, the launch, the status."""
+    dev, made = kv.index, []
+    po, pe = _arg(O, "O", BF16, (n, h, 128), dev), _arg(lse, "lse", F32, (n, h), dev)
+    pw, nw = _arg(ws, "ws", torch.uint8, None if ws is None else ws.shape, dev), 0 if ws is None else ws.numel()
+    _on_gpu(dev)
     if O is None:
         O = torch.empty_like(Q, memory_format=torch.contiguous_format)
+        po = O.data_ptr()
         made.append(O)
     if lse is None:
-        lse = Q.new_empty((Q.shape[0], Q.shape[1]), dtype=F32)
+        lse = Q.new_empty((n, h), dtype=F32)
+        pe = lse.data_ptr()
         made.append(lse)
-    if ws is None or ws.numel() < need:
-        ws = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
-        if need:
+    status = _launch(kv, stream, call, kv._ref, *args, po, pe, pw, nw)
+    if status == _lib.LSA_ENOSPACE:  # most calls need no workspace: asked for only now
+        size = need()
+        if nw < size:
+            ws = torch.empty((size,), dtype=torch.uint8, device=kv.device)
             made.append(ws)
-    return (O, lse, O.data_ptr(), lse.data_ptr(), None if ws is None else ws.data_ptr(),
-            0 if ws is None else ws.numel(), made)
+            status = _launch(kv, stream, call, kv._ref, *args, po, pe, ws.data_ptr(), size)
+    if status:
+        check(status, name)
+    if stream is not None:
+        for t in made:  # not to be reused before `stream` is done with them
+            t.record_stream(stream)
+    return O, lse
 
 
 def kv8_attn(Q: torch.Tensor, kv: KV8, table: torch.Tensor, lens: torch.Tensor, cu=None, sinks: int = 0,
@@ -767,30 +772,22 @@ def kv8_attn(Q: torch.Tensor, kv: KV8, table: torch.Tensor, lens: torch.Tensor, 
     """lsa_kv8_attn: attention of each sequence's newest tokens over the whole
     sequence (window > 0: over the last `window` positions and the first
     `sinks`).  Q [nq, hq, 128] bf16, sequence b's rows cu[b] .. cu[b + 1] - 1
-    (cu None: one each); lens counts the new tokens too.  Returns (O bf16
-    [nq, hq, 128], lse fp32 [nq, hq], base 2)."""
-    dev, L = kv.device, lib()
-    pq, ld = _rows(Q, "Q", None)
-    nq, hq, _ = Q.shape
-    if table.dim() != 2:
-        _spec(table, "table", I32, (None, None))
-    pt = _arg(table, "table", I32, table.shape)
-    n_seq, max_pages = table.shape
-    pl = _arg(lens, "lens", I32, (n_seq,))
-    pc = _arg(cu, "cu", I32, (n_seq + 1,))
-    _arg(O, "O", BF16, (nq, hq, 128))
-    _arg(lse, "lse", F32, (nq, hq))
-    _arg(ws, "ws", torch.uint8, (None,))
+    (cu None: one each); lens counts the new tokens too.  ws: optional, uint8,
+    used if it is large enough.  Returns (O bf16 [nq, hq, 128], lse fp32
+    [nq, hq], base 2)."""
+    dev, L = kv.index, lib()
+    pq, ld, nq, hq = _rows(Q, "Q", None, dev)
+    shape = table.shape
+    pt = _arg(table, "table", I32, shape if len(shape) == 2 else (None, None), dev)
+    n_seq, max_pages = shape
+    pl = _arg(lens, "lens", I32, (n_seq,), dev)
+    pc = _arg(cu, "cu", I32, (n_seq + 1,), dev)
     if cu is None and nq != n_seq:
         raise ValueError(f"Q: without cu, expected one row for each of {n_seq} sequences, got {nq}")
-    _on(dev, Q, table, lens, cu, O, lse, ws)
-    O, lse, po, pe, pw, nw, made = _kv8_buffers(dev, Q, O, lse, ws,
-                                                L.lsa_kv8_attn_workspace_bytes(kv._ref, nq, hq, cu is None, n_seq, max_pages,
-                                                                               sinks, window))
-    _launch(kv, stream, "lsa_kv8_attn",
-            lambda s: L.lsa_kv8_attn(kv._ref, pq, ld, nq, hq, pc, pt, pl, n_seq, max_pages, sinks, window, po, pe, pw,
-                                     nw, s), *made)
-    return O, lse
+    return _kv8_attend(kv, "lsa_kv8_attn", L.lsa_kv8_attn,
+                       (pq, ld, nq, hq, pc, pt, pl, n_seq, max_pages, sinks, window),
+                       lambda: kv8_attn_workspace_bytes(kv, nq, hq, n_seq, max_pages, cu is None, sinks, window),
+                       Q, nq, hq, O, lse, ws, stream)
 
 
 def kv8_sparse_attn(Q: torch.Tensor, kv: KV8, table: torch.Tensor, lens: torch.Tensor, idx: torch.Tensor, seq=None,
@@ -799,47 +796,47 @@ def kv8_sparse_attn(Q: torch.Tensor, kv: KV8, table: torch.Tensor, lens: torch.T
     idx [nq, hkv, n_idx] int32 positions in the query's sequence seq[i] (seq
     None: query i is sequence i's), -1 = padding.  Returns (O bf16
     [nq, hq, 128], lse fp32 [nq, hq], base 2)."""
-    dev, L = kv.device, lib()
-    pq, ld = _rows(Q, "Q", None)
-    nq, hq, _ = Q.shape
-    if table.dim() != 2:
-        _spec(table, "table", I32, (None, None))
-    pt = _arg(table, "table", I32, table.shape)
-    n_seq, max_pages = table.shape
-    pl = _arg(lens, "lens", I32, (n_seq,))
-    pi = _arg(idx, "idx", I32, (nq, kv.hkv, None))
-    pb = _arg(seq, "seq", I32, (nq,))
-    _arg(O, "O", BF16, (nq, hq, 128))
-    _arg(lse, "lse", F32, (nq, hq))
-    _arg(ws, "ws", torch.uint8, (None,))
+    dev, L = kv.index, lib()
+    pq, ld, nq, hq = _rows(Q, "Q", None, dev)
+    shape = table.shape
+    pt = _arg(table, "table", I32, shape if len(shape) == 2 else (None, None), dev)
+    n_seq, max_pages = shape
+    pl = _arg(lens, "lens", I32, (n_seq,), dev)
+    shape = idx.shape
+    n_idx = shape[2] if len(shape) == 3 else None
+    pi = _arg(idx, "idx", I32, (nq, kv.hkv, n_idx), dev)
+    pb = _arg(seq, "seq", I32, (nq,), dev)
     if seq is None and nq != n_seq:
         raise ValueError(f"Q: without seq, expected one row for each of {n_seq} sequences, got {nq}")
-    _on(dev, Q, table, lens, idx, seq, O, lse, ws)
-    n_idx = idx.shape[2]
-    O, lse, po, pe, pw, nw, made = _kv8_buffers(dev, Q, O, lse, ws,
-                                                L.lsa_kv8_sparse_attn_workspace_bytes(kv._ref, nq, hq, n_idx))
-    _launch(kv, stream, "lsa_kv8_sparse_attn",
-            lambda s: L.lsa_kv8_sparse_attn(kv._ref, pq, ld, nq, hq, pb, pt, pl, n_seq, max_pages, pi, n_idx, po, pe,
-                                            pw, nw, s), *made)
-    return O, lse
+    return _kv8_attend(kv, "lsa_kv8_sparse_attn", L.lsa_kv8_sparse_attn,
+                       (pq, ld, nq, hq, pb, pt, pl, n_seq, max_pages, pi, n_idx),
+                       lambda: kv8_sparse_attn_workspace_bytes(kv, nq, hq, n_idx), Q, nq, hq, O, lse, ws, stream)
+
+
+def _page_list(x, name, n_pages):
+    if not (isinstance(x, np.ndarray) and x.dtype == np.int32 and x.flags.c_contiguous):
+        x = np.asarray(x)
+        if x.size and x.dtype.kind not in "iu":
+            raise ValueError(f"{name}: expected a list of page numbers, got {x.dtype}")
+        if x.size and (x.min() < 0 or x.max() >= n_pages):
+            raise ValueError(f"{name}: page numbers must be in [0, {n_pages})")
+        x = np.ascontiguousarray(x, dtype=np.int32)
+    if x.ndim != 1:
+        raise ValueError(f"{name}: expected a list of page numbers, got shape {x.shape}")
+    return x
 
 
 def kv8_copy_pages(kv: KV8, src, dst, stream=None) -> KV8:
     """lsa_kv8_copy_pages: page src[i] onto page dst[i] (host sequences of page
     numbers; no page may be written twice, or both read and written)."""
-    pair = []
-    for name, x in (("src", src), ("dst", dst)):
-        x = np.asarray(x)
-        if x.ndim != 1 or (x.size and x.dtype.kind not in "iu"):
-            raise ValueError(f"{name}: expected a list of page numbers, got shape {x.shape} of {x.dtype}")
-        if x.dtype != np.int32 and x.size and (x.min() < 0 or x.max() >= kv.n_pages):
-            raise ValueError(f"{name}: page numbers must be in [0, {kv.n_pages})")
-        pair.append(np.ascontiguousarray(x, dtype=np.int32))
-    src, dst = pair
-    if src.size != dst.size:
-        raise ValueError(f"src and dst: expected two lists of one length, got {src.size} and {dst.size}")
-    ps, pd, n = src.__array_interface__["data"][0], dst.__array_interface__["data"][0], src.size
-    _launch(kv, stream, "lsa_kv8_copy_pages", lambda s: lib().lsa_kv8_copy_pages(kv._ref, ps, pd, n, s))
+    src, dst = _page_list(src, "src", kv.n_pages), _page_list(dst, "dst", kv.n_pages)
+    n = src.shape[0]
+    if dst.shape[0] != n:
+        raise ValueError(f"src and dst: expected two lists of one length, got {n} and {dst.shape[0]}")
+    status = _launch(kv, stream, lib().lsa_kv8_copy_pages, kv._ref, src.__array_interface__["data"][0],
+                     dst.__array_interface__["data"][0], n)
+    if status:
+        check(status, "lsa_kv8_copy_pages")
     return kv
 
 
