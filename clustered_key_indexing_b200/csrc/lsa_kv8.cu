@@ -67,8 +67,9 @@ __device__ __forceinline__ void kv8_unpack4(uint32_t w, float (&x)[4]) {
 constexpr int kKv8Warps = 8;  // warps of a CTA
 
 // Sum of v over the CTA's threads before this one, and over all of them.
+template <int WARPS = kKv8Warps>
 __device__ __forceinline__ long long kv8_block_scan(long long v, long long& all) {
-    __shared__ long long wsum[kKv8Warps];
+    __shared__ long long wsum[WARPS];
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     long long inc = v;
 #pragma unroll
@@ -81,7 +82,7 @@ __device__ __forceinline__ long long kv8_block_scan(long long v, long long& all)
     long long before = inc - v;
     all = 0;
 #pragma unroll
-    for (int i = 0; i < kKv8Warps; ++i) {
+    for (int i = 0; i < WARPS; ++i) {
         if (i < wid) before += wsum[i];
         all += wsum[i];
     }

@@ -56,7 +56,7 @@ struct Kv8AttnArgs {
     uint16_t* O;           // [nq, hq, 128]
     float* lse;            // [nq, hq] or NULL
     float* part;           // split rows' partial states
-    int32_t rows_per_seq;  // > 0: a CTA for each row, so many for each sequence
+    int32_t own;           // a CTA for each row: 1 sequences have one row a kv-head, 2 rows by the scan
     float scale_log2;
 };
 
@@ -645,7 +645,7 @@ __global__ void __launch_bounds__(32 * kKv8ListWarps, 2) kv8_list_kernel(Kv8Attn
 // it began before the CTA, slot 1 if it began inside), and kv8_join_kernel
 // joins them.  Everyone derives the stream from lens and cu by the same scan.
 // Where the call's shapes alone say that every row is short, each row gets a
-// CTA of its own instead (rows_per_seq > 0): no scan, no second kernel.
+// CTA of its own instead (own > 0): no second kernel, no workspace.
 struct Kv8Seq {
     int64_t base;     // first chunk of the sequence in the stream
     int32_t chunks;   // chunks of each of its rows
@@ -685,29 +685,30 @@ __device__ __forceinline__ void kv8_seq(const Kv8AttnArgs& a, int64_t b, Kv8Seq&
     }
 }
 
-template <int NT, bool LIST>
+// A sequence's share of a stream: its chunks, or (ROWS) its rows.
+template <int NT, bool LIST, int WARPS = kKv8Warps, bool ROWS = false>
 struct Kv8Scan {
     int64_t total, per;
-    long long begin, count, round;  // this thread's sequence in the first round of 256: its place, its chunks; the round's
+    long long begin, count, round;  // this thread's sequence in the CTA's first round: its place, its share; the round's
 
-    __device__ __forceinline__ long long chunks_of(const Kv8AttnArgs& a, int64_t b) const {
+    __device__ __forceinline__ long long share_of(const Kv8AttnArgs& a, int64_t b) const {
         if (b >= a.n_seq) return 0;
         Kv8Seq q;
         kv8_seq<NT, LIST>(a, b, q);
-        return (int64_t)q.chunks * q.rows;
+        return ROWS ? q.rows : (int64_t)q.chunks * q.rows;
     }
-    // Chunks of all sequences and each CTA's share of them (`least`: chunks a
-    // CTA takes at least).
+    // The stream's length and each CTA's share of it (`least`: a CTA takes at
+    // least so much).
     __device__ __forceinline__ void init(const Kv8AttnArgs& a, int n_cta, int least) {
         if constexpr (LIST) {
             total = a.nq * a.hkv * (int64_t)max(1, (a.n_idx + 31) / 32);
         } else {
-            count = chunks_of(a, threadIdx.x);
-            begin = kv8_block_scan(count, round);
+            count = share_of(a, threadIdx.x);
+            begin = kv8_block_scan<WARPS>(count, round);
             total = round;
-            for (int64_t b0 = 32 * kKv8Warps; b0 < a.n_seq; b0 += 32 * kKv8Warps) {
+            for (int64_t b0 = 32 * WARPS; b0 < a.n_seq; b0 += 32 * WARPS) {
                 long long all;
-                kv8_block_scan(chunks_of(a, b0 + threadIdx.x), all);
+                kv8_block_scan<WARPS>(share_of(a, b0 + threadIdx.x), all);
                 total += all;
             }
         }
@@ -717,7 +718,7 @@ struct Kv8Scan {
         const int64_t few = total < rows * least ? max((int64_t)1, (total + rows - 1) / rows) : least;
         per = max(few, (total + n_cta - 1) / n_cta);
     }
-    // The sequence whose chunks hold position w of the stream (0 <= w < total).
+    // The sequence that holds position w of the stream (0 <= w < total).
     __device__ __forceinline__ int64_t find(const Kv8AttnArgs& a, int64_t w, Kv8Seq& out) {
         int64_t b, base;
         if constexpr (LIST) {
@@ -729,9 +730,9 @@ struct Kv8Scan {
             b = threadIdx.x;
             while (w >= end) {  // uniform
                 long long all;
-                b += 32 * kKv8Warps;
-                m = chunks_of(a, b);
-                first = end + kv8_block_scan(m, all);
+                b += 32 * WARPS;
+                m = share_of(a, b);
+                first = end + kv8_block_scan<WARPS>(m, all);
                 end += all;
             }
             if (w >= first && w < first + m) { found[0] = b; found[1] = first; }
@@ -778,11 +779,20 @@ __global__ void __launch_bounds__(32 * WARPS, NT == 1 && WARPS == 8 ? 2 : 1) kv8
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, gq = lane >> 2, tq = lane & 3;
     Kv8Seq q;
     int64_t b, w0, w1;
-    if (WARPS != kKv8Warps || a.rows_per_seq > 0) {  // a CTA for each row
-        b = blockIdx.x / a.rows_per_seq;
-        const int r = blockIdx.x % a.rows_per_seq;
-        kv8_seq<NT, LIST>(a, b, q);
-        if (r >= q.rows) return;
+    if (WARPS != kKv8Warps || a.own) {  // a CTA for each row
+        int r;
+        if (LIST || a.own == 1) {
+            b = blockIdx.x / a.hkv;
+            r = blockIdx.x % a.hkv;
+            kv8_seq<NT, LIST>(a, b, q);
+            if (q.rows == 0) return;
+        } else {
+            Kv8Scan<NT, LIST, WARPS, true> scan;
+            scan.init(a, (int)gridDim.x, 1);
+            if (blockIdx.x >= scan.total) return;
+            b = scan.find(a, blockIdx.x, q);
+            r = (int)(blockIdx.x - q.base);
+        }
         q.base = 0;
         w0 = (int64_t)r * q.chunks;
         w1 = w0 + q.chunks;
@@ -992,12 +1002,12 @@ static int kv8_ctas() { return num_sms() * (NT == 1 ? 2 : 1); }
 static int kv8_nt(int64_t nq, int64_t n_seq, int G) { return nq * G > 8 * n_seq ? 2 : 1; }
 
 // How a call's rows meet the GPU: one warp a row (lists only), one CTA a row
-// (n > 0 of them for each sequence), or the stream (n = 0).  It goes by what
-// the host knows: the numbers of rows and an upper bound of a row's chunks.
+// (rows > 0 of them at most), or the stream (rows = 0).  It goes by what the
+// host knows: the numbers of rows and an upper bound of a row's chunks.
 struct Kv8Plan {
     int nt;
     bool warps;
-    int64_t rows_per_seq;
+    int64_t rows;
     size_t ws;
 };
 
@@ -1011,10 +1021,9 @@ static Kv8Plan kv8_plan(bool lists, int64_t nq, int64_t n_seq, int G, int32_t hk
     // 30 / 23, 1024 rows 33 / 42; 7 chunks, 512 rows 12 / 13
     p.warps = lists && (nq * hkv >= 4 * ctas || (nq * hkv >= 2 * ctas && max_chunks <= 32));
     if (p.warps) return p;
-    // one sequence can have all new tokens
-    const int64_t rows = hkv * (lists || one_each ? 1 : ceil_div<int64_t>(nq * G, 8 * p.nt));
-    // CTAs without a row exit at once, but not for free: at most four a CTA of the stream
-    if (max_chunks <= kv8_own_chunks(rows * n_seq) && rows * n_seq <= 4 * ctas) p.rows_per_seq = rows;
+    // a sequence's last group of columns may be a part
+    const int64_t rows = lists || one_each ? nq * hkv : hkv * (nq * G / (8 * p.nt) + n_seq);
+    if (max_chunks <= kv8_own_chunks(rows) && rows <= INT32_MAX) p.rows = rows;
     else p.ws = (size_t)ctas * 2 * (p.nt == 1 ? kv8_part_floats<1>() : kv8_part_floats<2>()) * sizeof(float);
     return p;
 }
@@ -1051,12 +1060,11 @@ static lsa_status launch_kv8_ctas(const Kv8AttnArgs& a, int n, cudaStream_t st) 
 
 template <int FMT, int NT, bool LIST>
 static lsa_status launch_kv8_split(Kv8AttnArgs a, const Kv8Plan& p, int64_t n_seq, bool one_each, cudaStream_t st) {
-    a.rows_per_seq = (int32_t)p.rows_per_seq;
-    if (p.rows_per_seq > 0) {
-        const int rows = (int)(p.rows_per_seq * n_seq);
+    if (p.rows > 0) {
+        a.own = LIST || one_each ? 1 : 2;
         if constexpr (NT == 1)
-            if (rows <= num_sms()) return launch_kv8_ctas<FMT, 1, LIST, 16>(a, rows, st);
-        return launch_kv8_ctas<FMT, NT, LIST, kKv8Warps>(a, rows, st);
+            if (p.rows <= num_sms()) return launch_kv8_ctas<FMT, 1, LIST, 16>(a, (int)p.rows, st);
+        return launch_kv8_ctas<FMT, NT, LIST, kKv8Warps>(a, (int)p.rows, st);
     }
     const int n = kv8_ctas<NT>();
     lsa_status s;
