@@ -754,7 +754,8 @@ def _kv8_attend(kv, name, call, args, need, Q, n, h, O, lse, ws, stream):
         made.append(lse)
     status = _launch(kv, stream, call, kv._ref, *args, po, pe, pw, nw)
     if status == _lib.LSA_ENOSPACE:  # most calls need no workspace: asked for only now
-        size = need()
+        with torch.cuda.device(kv.device):
+            size = need()
         if nw < size:
             ws = torch.empty((size,), dtype=torch.uint8, device=kv.device)
             made.append(ws)

@@ -659,7 +659,8 @@ lsa_status lsa_kv8_write(const lsa_kv8* kv, const uint16_t* K, int64_t k_stride,
                          int32_t n_seq, int32_t max_pages, void* stream);
 
 /* Workspace bytes of lsa_kv8_attn (one_each: cu is NULL) and of
- * lsa_kv8_sparse_attn for the same sizes; 0 where none is needed. */
+ * lsa_kv8_sparse_attn for the same sizes on the current device; 0 where none
+ * is needed. */
 size_t lsa_kv8_attn_workspace_bytes(const lsa_kv8* kv, int64_t nq, int32_t hq, int32_t one_each,
                                     int32_t n_seq, int32_t max_pages, int32_t sinks,
                                     int32_t window);
@@ -676,7 +677,8 @@ size_t lsa_kv8_sparse_attn_workspace_bytes(const lsa_kv8* kv, int64_t nq, int32_
  * token rows q_stride elements apart (a multiple of 8); O [nq, hq, d_head]
  * bf16; lse (may be NULL) [nq, hq] fp32, the base-2 log-sum-exp of the scores
  * scaled by log2(e) / sqrt(d_head).  A row with no key gives O = 0 and lse =
- * -inf.  Every group of 8 (16, when sequences have more than 8 on average)
+ * -inf; rows of Q that no sequence claims are not computed (O and lse keep what
+ * they held).  Every group of 8 (16, when sequences have more than 8 on average)
  * columns -- (new token, query head of one kv-head) pairs -- reads the cache
  * once: made for decoded and drafted tokens, not for whole prompts.
  * ws: lsa_kv8_attn_workspace_bytes(), 16-byte aligned; calls that may run at
