@@ -618,7 +618,8 @@ class KV8:
             raise ValueError("LSA calls take CUDA tensors (there is no CPU implementation)")
         shape = (n_pages, hkv, page, 128)
         K, V = (torch.zeros(shape, dtype=torch.uint8, device=device).view(KV8_DTYPES[fmt]) for _ in range(2))
-        self._wrap(K, V, torch.full((n_pages, hkv, 2), 2.0 ** -100, dtype=F32, device=device))
+        scale = torch.full((n_pages, hkv, 2), 2.0 ** -100, dtype=F32, device=device)
+        self._wrap(K, V, scale, K.data_ptr(), V.data_ptr(), scale.data_ptr(), K.get_device())
 
     @classmethod
     def of(cls, K: torch.Tensor, V: torch.Tensor, scale: torch.Tensor) -> "KV8":
@@ -630,22 +631,26 @@ class KV8:
             raise ValueError(f"K: expected shape ('*', '*', '*', 128), got {tuple(shape)}")
         if shape[2] not in KV8_PAGES:
             raise ValueError(f"page: expected one of {KV8_PAGES}, got {shape[2]}")
-        _arg(K, "K", dtype, shape, dev)
-        _arg(V, "V", dtype, shape, dev)
-        _arg(scale, "scale", F32, (shape[0], shape[1], 2), dev)
+        pk, pv = _arg(K, "K", dtype, shape, dev), _arg(V, "V", dtype, shape, dev)
+        ps = _arg(scale, "scale", F32, (shape[0], shape[1], 2), dev)
         _on_gpu(dev)
         kv = cls.__new__(cls)
-        kv._wrap(K, V, scale)
+        kv._wrap(K, V, scale, pk, pv, ps, dev)
         return kv
 
-    def _wrap(self, K, V, scale):
-        self.K, self.V, self.scale = K, V, scale
+    def _wrap(self, K, V, scale, pk, pv, ps, dev):
+        self.K, self.V, self.scale, self.index = K, V, scale, dev
         self.n_pages, self.hkv, self.page, _ = K.shape
-        code = KV8_FMT[K.dtype]
-        self.fmt = "int8" if code else "e4m3"
-        self.device, self.index = K.device, K.get_device()
-        self.c = _lib.lsa_kv8(code, self.hkv, self.page, self.n_pages, K.data_ptr(), V.data_ptr(), scale.data_ptr())
+        self.c = _lib.lsa_kv8(KV8_FMT[K.dtype], self.hkv, self.page, self.n_pages, pk, pv, ps)
         self._ref = ctypes.byref(self.c)
+
+    @property
+    def fmt(self) -> str:
+        return "int8" if self.c.fmt else "e4m3"
+
+    @property
+    def device(self) -> torch.device:
+        return self.K.device
 
 
 # The calls below serve single decoded tokens, where a call's time is what the
@@ -696,7 +701,7 @@ def _launch(kv, stream, call, *args):
     """call(*args, stream handle) with the cache's device current; its status."""
     dev = kv.index
     _on_gpu(dev)
-    if torch.cuda.current_device() != dev:
+    if torch._C._cuda_getDevice() != dev:
         with torch.cuda.device(dev):
             return _launch(kv, stream, call, *args)
     return call(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)

@@ -20,7 +20,8 @@ def z(*shape, dtype=bf16):
 def fake_cache(hkv=2, page=16, n_pages=4):
     """A KV8 over CPU arrays: its checks run, no call gets past them."""
     kv = lsa.KV8.__new__(lsa.KV8)
-    kv._wrap(z(n_pages, hkv, page, 128, dtype=i8), z(n_pages, hkv, page, 128, dtype=i8), z(n_pages, hkv, 2, dtype=f32))
+    K, V, scale = z(n_pages, hkv, page, 128, dtype=i8), z(n_pages, hkv, page, 128, dtype=i8), z(n_pages, hkv, 2, dtype=f32)
+    kv._wrap(K, V, scale, K.data_ptr(), V.data_ptr(), scale.data_ptr(), K.get_device())
     return kv
 
 
