@@ -186,10 +186,10 @@ __device__ __forceinline__ void kv8_scores(const Kv8State<NT>& s, const Kv8K& k,
         for (int i = 0; i < 4; ++i) sc[nt][i] = c[nt][0][i] + c[nt][1][i];
 }
 
-// V^T of a step as ldmatrix transposes it: register 2 i (+ 1) of the pair i / 2
-// holds dim 8 i + g (of 16 i..: see kv8_read_v) of keys 4 t .. 4 t + 3.
+// V^T of a step as the transposing 8-bit ldmatrix delivers it: the codes of keys
+// 4 t .. 4 t + 3 in dims 16 mt + g (w[2 mt]) and 16 mt + g + 8 (w[2 mt + 1]).
 struct Kv8V {
-    uint32_t w[16];  // w[2 mt], w[2 mt + 1]: dims 16 mt + g and 16 mt + g + 8
+    uint32_t w[16];
 };
 
 // O^T += V^T P^T: keys 4 t, 4 t + 1 are the MMA's k = 2 t, 2 t + 1 and keys
@@ -367,7 +367,7 @@ constexpr int kKv8Step = 16 * kD;                       // bytes of K (or V) in 
 constexpr int kKv8Note = 32 * 8 + 32 * 4;               // a chunk's scales (float2) and rows, beside the ring
 constexpr int kKv8Ring = kKv8Stages * 2 * kKv8Step;     // bytes of a warp's ring ...
 constexpr int kKv8Warp = kKv8Ring + 2 * kKv8Note + 256; // ... and of all it has (a multiple of 1024)
-static_assert(kKv8Warp % 1024 == 0, "the ring's swizzle goes by address");
+static_assert(kKv8Warp % 1024 == 0, "rings start on a swizzle's period");
 
 // Where this lane's copies come from and go to.
 struct Kv8Copy {
@@ -536,9 +536,10 @@ __device__ __forceinline__ void kv8_step(const Kv8AttnArgs& a, const Kv8Keys<LIS
     kv8_pv<FMT, NT>(s, v, pb);
 }
 
-// Chunks c, c + STEP, ... below cend of a row into the warp's state.  Copies run two steps ahead
-// of their use, table entries and scales a chunk further, list entries two.
-// start() brings the first chunk on its way, so that Q can be read meanwhile.
+// Chunks c, c + STEP, ... below cend of a row into the warp's state.  Copies
+// run two steps ahead of their use, page numbers and scales a chunk further,
+// list entries two.  start() sends the first chunk on its way, so that Q can be
+// read meanwhile.
 template <bool LIST, int STEP>
 struct Kv8Walk {
     Kv8Copy cp;
