@@ -745,31 +745,37 @@ def kv8_sparse_attn_workspace_bytes(kv: KV8, nq: int, hq: int, n_idx: int) -> in
 def _kv8_attend(kv, name, call, args, need, Q, n, h, O, lse, ws, stream):
     """The tail of both attention calls: outputs and workspace that the caller
     gave or that are made here, the launch, the status."""
-    dev, made = kv.index, []
+    dev = kv.index
+    if stream is not None:
+        if stream.device_index != dev:
+            raise ValueError(f"stream: expected one of device {dev}, got one of device {stream.device_index}")
+        # what is made here is `stream`'s memory: a block that the current stream
+        # gave back may still be in use there
+        here = torch.cuda.current_stream(dev)
+        with torch.cuda.stream(stream):
+            out = _kv8_attend(kv, name, call, args, need, Q, n, h, O, lse, ws, None)
+        for t, given in zip(out, (O, lse)):
+            if given is None and here != stream:
+                t.record_stream(here)
+        return out
     po, pe = _arg(O, "O", BF16, (n, h, 128), dev), _arg(lse, "lse", F32, (n, h), dev)
     pw, nw = _arg(ws, "ws", torch.uint8, None if ws is None else ws.shape, dev), 0 if ws is None else ws.numel()
     _on_gpu(dev)
     if O is None:
         O = torch.empty_like(Q, memory_format=torch.contiguous_format)
         po = O.data_ptr()
-        made.append(O)
     if lse is None:
         lse = Q.new_empty((n, h), dtype=F32)
         pe = lse.data_ptr()
-        made.append(lse)
-    status = _launch(kv, stream, call, kv._ref, *args, po, pe, pw, nw)
+    status = _launch(kv, None, call, kv._ref, *args, po, pe, pw, nw)
     if status == _lib.LSA_ENOSPACE:  # most calls need no workspace: asked for only now
         with torch.cuda.device(kv.device):
             size = need()
         if nw < size:
             ws = torch.empty((size,), dtype=torch.uint8, device=kv.device)
-            made.append(ws)
-            status = _launch(kv, stream, call, kv._ref, *args, po, pe, ws.data_ptr(), size)
+            status = _launch(kv, None, call, kv._ref, *args, po, pe, ws.data_ptr(), size)
     if status:
         check(status, name)
-    if stream is not None:
-        for t in made:  # not to be reused before `stream` is done with them
-            t.record_stream(stream)
     return O, lse
 
 

@@ -1156,7 +1156,8 @@ lsa_status lsa_kv8_attn(const lsa_kv8* kv, const uint16_t* Q, int64_t q_stride, 
     if (!cu && nq != n_seq) return set_error(LSA_EINVAL, "lsa_kv8_attn: without cu, nq must equal n_seq");
     if (nq == 0) return LSA_OK;
     Kv8AttnArgs a = kv8_args(kv, Q, q_stride, nq, hq, table, lens, n_seq, max_pages, O, lse, ws);
-    a.cu = cu; a.S = window > 0 ? sinks : 0; a.W = window;
+    // a window as long as the longest sequence hides nothing
+    a.cu = cu; a.W = window < (int64_t)max_pages * kv->page ? window : 0; a.S = a.W > 0 ? sinks : 0;
     const Kv8Plan p = kv8_plan(false, nq, n_seq, a.G, kv->hkv, cu == nullptr,
                                kv8_max_chunks(nq, kv->page, max_pages, sinks, window));
     if (p.ws > 0 && (!ws || ws_bytes < p.ws)) return set_error(LSA_ENOSPACE, "lsa_kv8_attn: workspace too small");

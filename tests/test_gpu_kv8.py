@@ -466,6 +466,35 @@ def test_another_stream(lsa):
     assert r[0] is O and r[1] is lse and torch.equal(O, want[0]) and torch.equal(lse, want[1])
 
 
+def test_outputs_made_for_a_stream_are_its_own_memory(lsa):
+    """A block that the current stream gave back may still be read there, so a
+    call on another stream does not take it."""
+    rng = np.random.default_rng(34)
+    kv, table, lens, idx = small_case(lsa, rng)
+    q = bf16(rng.standard_normal((3, 8, 128)))[0]
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for call in (lambda: lsa.kv8_attn(q, kv, table, lens, stream=s), lambda: lsa.kv8_sparse_attn(q, kv, table, lens, idx, stream=s)):
+        used = [torch.empty_like(q) for _ in range(3)] + [torch.empty(3, 8, device="cuda") for _ in range(3)]
+        places = {x.data_ptr() for x in used}
+        del used
+        assert not places & {x.data_ptr() for x in call()}
+    torch.cuda.synchronize()
+
+
+def test_a_window_longer_than_everything(lsa):
+    """The same as none, for queries before the first token too."""
+    rng = np.random.default_rng(35)
+    kv, table = filled(lsa, rng, [2, 90], 2, 16, "e4m3")
+    q = bf16(rng.standard_normal((12, 4, 128)))[0]
+    cu, lens = i32([0, 9, 12]), i32([2, 90])
+    want = lsa.kv8_attn(q, kv, i32(table), lens, cu=cu)
+    for window in (table.shape[1] * 16, 2 ** 31 - 1):
+        got = lsa.kv8_attn(q, kv, i32(table), lens, cu=cu, sinks=3, window=window)
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+    lsa.check_device_error()
+
+
 def test_bad_pages_and_ranges_are_reported(lsa):
     from clustered_key_indexing_b200._lib import LSA_EDEVICE, LSAError
 
