@@ -14,6 +14,8 @@
 #include <stdint.h>
 #include <stdlib.h>
 
+#include <algorithm>
+
 #include "lsa_common.cuh"
 #include "lsa_mma.cuh"
 
@@ -302,34 +304,45 @@ __global__ void __launch_bounds__(256, PASSES <= 8 ? 5 : 2) kv8_write_kernel(Kv8
 }
 
 // Page copies.  The pairs travel in the launch's own arguments: no upload, and
-// a captured launch keeps them.  One CTA moves 16 KB of one page's K or V;
-// the first CTA of a page also moves its scales.
+// a captured launch keeps them; up to 4000 a launch (2000 at a time cost 4 to 8
+// us more for 4096).  One CTA moves 16 KB: a part of one page's K or V, or of
+// small pages as many as fit (4000 pairs of 2 KB: 8.1 us, 10.1 with a CTA for
+// each); the CTA with a page's first part also moves its scales.  4096 pages of
+// 64 tokens and 8 heads (0.54 GB read and written) take 168 us on the GPU, 6.4 TB/s;
+// a CTA's share of 8 to 64 KB, or cached loads and stores, change it by 2%.
 template <int N>
 struct Kv8Pairs {
     int32_t src[N], dst[N];
 };
 
-constexpr int kCopyChunk = 16384;
+constexpr int kCopyUnits = 1024;  // 16-byte units a CTA moves
 
+// upp: units of a page; per: pages of a CTA; nchunk: CTAs of a page (one of the two is 1)
 template <int N>
-__global__ void __launch_bounds__(256) kv8_copy_kernel(const __grid_constant__ Kv8Pairs<N> p, uint8_t* K, uint8_t* V,
-                                                       float* scale, int64_t page_bytes, int32_t nchunk, int32_t hkv) {
-    const int i = blockIdx.x / nchunk, ch = blockIdx.x % nchunk;
-    uint8_t* pool = blockIdx.y ? V : K;
-    const int64_t s = p.src[i], d = p.dst[i];
-    const uint4* from = reinterpret_cast<const uint4*>(pool + s * page_bytes);
-    uint4* to = reinterpret_cast<uint4*>(pool + d * page_bytes);
-    const int64_t n = page_bytes / 16;
-    const int64_t at = (int64_t)ch * (kCopyChunk / 16) + threadIdx.x;
+__global__ void __launch_bounds__(256) kv8_copy_kernel(const __grid_constant__ Kv8Pairs<N> p, uint4* K, uint4* V,
+                                                       float* scale, int n, uint32_t upp, int per, int nchunk, int hkv) {
+    const int i0 = blockIdx.x / nchunk * per, ch = blockIdx.x % nchunk;
+    uint4* pool = blockIdx.y ? V : K;
+    const int cnt = min(per, n - i0);
     uint4 x[4];
+    uint4* to[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const uint32_t at = ch * (uint32_t)kCopyUnits + 256 * u + threadIdx.x, j = at / upp;
+        to[u] = nullptr;
+        if (j < (uint32_t)cnt) {
+            x[u] = __ldcs(pool + p.src[i0 + j] * (int64_t)upp + (at - j * upp));
+            to[u] = pool + p.dst[i0 + j] * (int64_t)upp + (at - j * upp);
+        }
+    }
 #pragma unroll
     for (int u = 0; u < 4; ++u)
-        if (at + 256 * u < n) x[u] = __ldcs(from + at + 256 * u);
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-        if (at + 256 * u < n) __stcs(to + at + 256 * u, x[u]);
+        if (to[u]) __stcs(to[u], x[u]);
     if (ch == 0 && blockIdx.y == 0)
-        for (int j = threadIdx.x; j < 2 * hkv; j += 256) scale[d * 2 * hkv + j] = scale[s * 2 * hkv + j];
+        for (int e = threadIdx.x; e < cnt * 2 * hkv; e += 256) {
+            const int j = e / (2 * hkv), h = e % (2 * hkv);
+            scale[p.dst[i0 + j] * (int64_t)(2 * hkv) + h] = scale[p.src[i0 + j] * (int64_t)(2 * hkv) + h];
+        }
 }
 
 static lsa_status check_kv8(const lsa_kv8* c) {
@@ -384,9 +397,10 @@ template <int N>
 static void launch_kv8_copy(const lsa_kv8* c, const int32_t* src, const int32_t* dst, int n, cudaStream_t st) {
     Kv8Pairs<N> p;
     for (int i = 0; i < n; ++i) { p.src[i] = src[i]; p.dst[i] = dst[i]; }
-    const int64_t bytes = (int64_t)c->hkv * c->page * kD;
-    const int nchunk = (int)ceil_div<int64_t>(bytes, kCopyChunk);
-    kv8_copy_kernel<N><<<dim3((unsigned)(n * nchunk), 2), 256, 0, st>>>(p, c->K, c->V, c->scale, bytes, nchunk, c->hkv);
+    const uint32_t upp = (uint32_t)c->hkv * c->page * (kD / 16);
+    const int per = std::max(1u, kCopyUnits / upp), nchunk = (int)ceil_div<int64_t>(upp, kCopyUnits);
+    kv8_copy_kernel<N><<<dim3((unsigned)(ceil_div(n, per) * nchunk), 2), 256, 0, st>>>(
+        p, reinterpret_cast<uint4*>(c->K), reinterpret_cast<uint4*>(c->V), c->scale, n, upp, per, nchunk, c->hkv);
 }
 
 }  // namespace lsa
@@ -444,7 +458,7 @@ lsa_status lsa_kv8_copy_pages(const lsa_kv8* kv, const int32_t* src, const int32
         return set_error(LSA_EINVAL, "lsa_kv8_copy_pages: pair %lld (%d -> %d): a page is written twice, or read and written",
                          (long long)bad, src[bad], dst[bad]);
     const cudaStream_t st = (cudaStream_t)stream;
-    constexpr int kFew = 60, kMany = 2000;  // 480 bytes or 16 KB of arguments
+    constexpr int kFew = 60, kMany = 4000;  // 480 bytes or 32 KB of arguments
     for (int64_t i = 0; i < n; i += kMany) {
         const int m = (int)(n - i < kMany ? n - i : kMany);
         {
