@@ -769,8 +769,11 @@ def _kv8_attend(kv, name, call, args, need, Q, n, h, O, lse, ws, stream):
         pe = lse.data_ptr()
     status = _launch(kv, None, call, kv._ref, *args, po, pe, pw, nw)
     if status == _lib.LSA_ENOSPACE:  # most calls need no workspace: asked for only now
-        with torch.cuda.device(kv.device):
+        if torch._C._cuda_getDevice() == dev:
             size = need()
+        else:
+            with torch.cuda.device(dev):
+                size = need()
         if nw < size:
             ws = torch.empty((size,), dtype=torch.uint8, device=kv.device)
             status = _launch(kv, None, call, kv._ref, *args, po, pe, ws.data_ptr(), size)

@@ -29,6 +29,7 @@
 #include <float.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "lsa_common.cuh"
@@ -652,7 +653,10 @@ __global__ void __launch_bounds__(32 * kKv8ListWarps, 2) kv8_list_kernel(Kv8Attn
 // it began before the CTA, slot 1 if it began inside), and kv8_join_kernel
 // joins them.  Everyone derives the stream from lens and cu by the same scan.
 // Where the call's shapes alone say that every row is short, each row gets a
-// CTA of its own instead (own > 0): no second kernel, no workspace.
+// CTA of its own instead (own > 0), or where rows are few a cluster of 2, 4 or 8,
+// whose CTAs take equal shares and join their sums through one another's shared
+// memory: no second kernel, no workspace.  8 rows of 282 chunks (9000 tokens):
+// 11.6 us, 16.7 in the stream (captured; called one by one 14.4 and 24.2).
 //
 // Bound by HBM: a million tokens of 8 kv-heads (2.15 GB) in 330 to 375 us, 32
 // sequences of 2K to 32K tokens (1.21 GB) in 205 us, 5.9 TB/s; the warps of a
@@ -779,34 +783,79 @@ __device__ __forceinline__ void kv8_store(const Kv8AttnArgs& a, int64_t orow, in
     if (d == 0 && a.lse) a.lse[orow] = any ? m - kKv8Head + log2f(l) : -CUDART_INF_F;
 }
 
-// WARPS = 16 (twice the steps at a time, one CTA an SM): only a CTA a row.
+// Number of this CTA in its cluster, CTAs of the cluster, the cluster's barrier
+// (which orders shared memory), and a load from CTA `rank`'s shared memory.
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_nctarank;\n" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_barrier() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t peer_smem(uint32_t p, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(p), "r"(rank));
+    return r;
+}
+
+__device__ __forceinline__ float4 peer_f4(uint32_t p) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];\n" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(p) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float2 peer_f2(uint32_t p) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];\n" : "=f"(v.x), "=f"(v.y) : "r"(p) : "memory");
+    return v;
+}
+
+// WARPS = 16 (twice the steps at a time, one CTA an SM): only a CTA or cluster a row.
 template <int FMT, int NT, bool LIST, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS, NT == 1 && WARPS == 8 ? 2 : 1) kv8_split_kernel(Kv8AttnArgs a, int least) {
     extern __shared__ __align__(1024) uint8_t ksm[];
+    constexpr bool CLUSTER = WARPS != kKv8Warps || NT == 2;  // may run as clusters
     __shared__ __align__(8) float sml[WARPS * 8 * NT * 2];                     // (m, l) of every warp's columns
+    __shared__ __align__(8) float cml[CLUSTER ? 8 * NT * 2 : 2];               // and of the CTA's, for its cluster
     const uint32_t ring = smem_u32(ksm) + (threadIdx.x >> 5) * kKv8Warp;
     // a warp's sums go where its ring was: [8 NT][kKv8Pad] floats
     auto so = [&](int w) { return reinterpret_cast<float*>(ksm + w * kKv8Warp); };
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, gq = lane >> 2, tq = lane & 3;
+    // a CTA's sums of column c, for its cluster: behind the sums in warp c % 8's ring
+    auto sc = [&](int c) { return ksm + (c & 7) * kKv8Warp + 8 * NT * kKv8Pad * 4 + (c >> 3) * kD * 4; };
+    static_assert(8 * NT * kKv8Pad * 4 + NT * kD * 4 <= kKv8Warp, "sums fit");
+    const bool own = WARPS != kKv8Warps || a.own;  // a CTA or a cluster for each row
+    const int csize = CLUSTER && own ? (int)cluster_size() : 1;
     Kv8Seq q;
-    int64_t b, w0, w1;
-    if (WARPS != kKv8Warps || a.own) {  // a CTA for each row
-        int r;
+    int64_t b, w0 = 0, w1 = 0;
+    int r = 0, t0 = 0, n = 0;  // row of the sequence, its first chunk here, how many
+    if (own) {
+        const int item = (int)(blockIdx.x / csize);
         if (LIST || a.own == 1) {
-            b = blockIdx.x / a.hkv;
-            r = blockIdx.x % a.hkv;
+            b = item / a.hkv;
+            r = item % a.hkv;
             kv8_seq<NT, LIST>(a, b, q);
             if (q.rows == 0) return;
         } else {
             Kv8Scan<NT, LIST, WARPS, true> scan;
             scan.init(a, (int)gridDim.x, 1);
-            if (blockIdx.x >= scan.total) return;
-            b = scan.find(a, blockIdx.x, q);
-            r = (int)(blockIdx.x - q.base);
+            if (item >= scan.total) return;
+            b = scan.find(a, item, q);
+            r = (int)(item - q.base);
         }
-        q.base = 0;
-        w0 = (int64_t)r * q.chunks;
-        w1 = w0 + q.chunks;
+        const int per = (q.chunks + csize - 1) / csize;
+        t0 = CLUSTER && csize > 1 ? (int)cluster_rank() * per : 0;
+        n = max(0, min(per, q.chunks - t0));
     } else {
         asm volatile("griddepcontrol.launch_dependents;\n");
         Kv8Scan<NT, LIST> scan;
@@ -816,17 +865,19 @@ __global__ void __launch_bounds__(32 * WARPS, NT == 1 && WARPS == 8 ? 2 : 1) kv8
         if (w0 >= w1) return;
         b = scan.find(a, w0, q);
     }
-    for (int64_t w = w0; w < w1;) {
-        while (w >= q.base + (int64_t)q.chunks * q.rows) {  // the next sequence that has rows
-            const int64_t next = q.base + (int64_t)q.chunks * q.rows;
-            kv8_seq<NT, LIST>(a, ++b, q);
-            q.base = next;
+    for (int64_t w = w0;;) {
+        if (!own) {
+            while (w >= q.base + (int64_t)q.chunks * q.rows) {  // the next sequence that has rows
+                const int64_t next = q.base + (int64_t)q.chunks * q.rows;
+                kv8_seq<NT, LIST>(a, ++b, q);
+                q.base = next;
+            }
+            const int64_t rel = w - q.base;
+            r = rel >> 31 ? (int)(rel / q.chunks) : (int)((uint32_t)rel / (uint32_t)q.chunks);
+            t0 = (int)(rel - (int64_t)r * q.chunks);
+            n = (int)min((int64_t)(q.chunks - t0), w1 - w);
         }
-        const int64_t rel = w - q.base;
-        const int r = rel >> 31 ? (int)(rel / q.chunks) : (int)((uint32_t)rel / (uint32_t)q.chunks);
-        const int t0 = (int)(rel - (int64_t)r * q.chunks);
         const int g = r / q.groups, cg = r % q.groups;
-        const int n = (int)min((int64_t)(q.chunks - t0), w1 - w);
         const int ta = t0 + wid, tb = t0 + n;  // neighbouring chunks at the same time: whole pages of DRAM
 
         if (ta < tb) {
@@ -906,15 +957,41 @@ __global__ void __launch_bounds__(32 * WARPS, NT == 1 && WARPS == 8 ? 2 : 1) kv8
                 l += ml.y * f;
                 acc = make_float4(acc.x + x.x * f, acc.y + x.y * f, acc.z + x.z * f, acc.w + x.w * f);
             }
-            if (final_) {
+            if (CLUSTER && csize > 1) {
+                *reinterpret_cast<float4*>(sc(c) + dim * 4) = acc;
+                if (dim == 0) *reinterpret_cast<float2*>(cml + 2 * c) = make_float2(M, l);
+            } else if (final_) {
                 kv8_store(a, orow, dim, acc, M, l);
             } else {
                 *reinterpret_cast<float4*>(part + c * kD + dim) = acc;
                 if (dim == 0) *reinterpret_cast<float2*>(part + 8 * NT * kD + 2 * c) = make_float2(M, l);
             }
         }
-        __syncthreads();
+        if (CLUSTER && csize > 1) {
+            cluster_barrier();
+            for (int e = (int)cluster_rank() * 32 * WARPS + tid; e < 8 * NT * kD / 4; e += csize * 32 * WARPS) {
+                const int c = e / (kD / 4), dim = e % (kD / 4) * 4;
+                const int64_t orow = kv8_out_row<NT>(a, q, cg, g, c);
+                if (orow < 0) continue;
+                float M = -FLT_MAX, l = 0.f;
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                const uint32_t pm = smem_u32(cml + 2 * c), ps = smem_u32(sc(c) + dim * 4);
+                for (int i = 0; i < csize; ++i) {
+                    const float2 ml = peer_f2(peer_smem(pm, i));
+                    const float4 x = peer_f4(peer_smem(ps, i));
+                    const float m = fmaxf(M, ml.x), fa = ex2(M - m), fb = ex2(ml.x - m);
+                    acc = make_float4(acc.x * fa + x.x * fb, acc.y * fa + x.y * fb, acc.z * fa + x.z * fb, acc.w * fa + x.w * fb);
+                    l = l * fa + ml.y * fb;
+                    M = m;
+                }
+                kv8_store(a, orow, dim, acc, M, l);
+            }
+            cluster_barrier();  // nobody leaves while others read its sums
+            return;
+        }
         w += n;
+        if (own || w >= w1) return;
+        __syncthreads();
     }
 }
 
@@ -998,43 +1075,90 @@ __global__ void __launch_bounds__(32 * kKv8Warps) kv8_join_kernel(Kv8AttnArgs a,
 // Chunks a CTA of the stream takes at least (one a warp).
 constexpr int kKv8Least = 8;
 
-// Chunks a row may have for a CTA of its own.  A row's CTA takes 4.5 us and
-// 2.2 us for each chunk of its warps; the stream takes 10 us before it wins by
-// spreading few rows over the GPU, and two pieces a CTA when rows are many.
-// Measured (own CTA / stream, us): 8 rows of 32 chunks 9.3 / 10.2, of 48 11.3 /
-// 10.4; 64 rows of 94 chunks 18.1 / 19.2, of 128 22.3 / 20.4; 128 rows of 128
-// chunks 26 / 33, of ragged lengths up to that 22 / 26; 512 rows of 128 89 / 94.
-static int64_t kv8_own_chunks(int64_t rows) { return rows < 104 ? 24 + rows : 128; }
-
 template <int NT>
 static int kv8_ctas() { return num_sms() * (NT == 1 ? 2 : 1); }
 
 // Columns per warp step: 16 when a sequence has on average more than 8.
 static int kv8_nt(int64_t nq, int64_t n_seq, int G) { return nq * G > 8 * n_seq ? 2 : 1; }
 
-// How a call's rows meet the GPU: one warp a row (lists only), one CTA a row
-// (rows > 0 of them at most), or the stream (rows = 0).  It goes by what the
-// host knows: the numbers of rows and an upper bound of a row's chunks.
+// A kernel's dynamic shared memory limit, raised once a device.
+static void kv8_allow_smem(const void* kern, size_t bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_acquire) & bit) return;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess)
+        done.fetch_or(bit, std::memory_order_release);
+}
+
+// Clusters of 2^lg CTAs (one an SM) that run at the same time: fewer than the SMs
+// make, because a cluster stays inside a group of SMs.  Asked once a device.
+static int kv8_clusters(int lg) {
+    static std::atomic<int> known[64][4];
+    static std::atomic<uint64_t> allowed{0};
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return num_sms() * 3 / 4 >> lg;
+    if (dev >= 0 && dev < 64 && (n = known[dev][lg].load(std::memory_order_relaxed)) > 0) return n;
+    const auto kern = kv8_split_kernel<0, 1, false, 16>;
+    constexpr size_t smem = 16 * kKv8Warp;
+    kv8_allow_smem((const void*)kern, smem, allowed);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(num_sms() >> lg << lg);
+    cfg.blockDim = dim3(512);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim = {1u << lg, 1u, 1u};
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) {
+        (void)cudaGetLastError();
+        n = num_sms() * 3 / 4 >> lg;
+    }
+    if (dev >= 0 && dev < 64) known[dev][lg].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+// Chunks a CTA may have of a row that is not in the stream, where `ctas` of them
+// run: a CTA takes 4.5 us and 2 us for a chunk of each of its 16 warps; the
+// stream 13 us, and then the same on all SMs (its shares are equal, so the cap
+// is for rows of unequal lengths).  More CTAs than SMs: 128.
+static int64_t kv8_cta_chunks(int64_t ctas) {
+    const int64_t n = num_sms();
+    return ctas > n ? 128 : std::min<int64_t>(160, 720 * n / (10 * n - 9 * ctas));
+}
+
+// How a call's rows meet the GPU: one warp a row (lists only), one CTA or
+// cluster a row (rows > 0 of them at most), or the stream (rows = 0).  It goes
+// by what the host knows: the numbers of rows and an upper bound of a row's
+// chunks.
 struct Kv8Plan {
     int nt;
     bool warps;
     int64_t rows;
+    int cluster;  // CTAs of a row
     size_t ws;
 };
 
 static Kv8Plan kv8_plan(bool lists, int64_t nq, int64_t n_seq, int G, int32_t hkv, bool one_each, int64_t max_chunks) {
     Kv8Plan p{};
     p.nt = lists ? 1 : kv8_nt(nq, n_seq, G);
-    const int ctas = p.nt == 1 ? kv8_ctas<1>() : kv8_ctas<2>();
+    p.cluster = 1;
+    const int ctas = p.nt == 1 ? kv8_ctas<1>() : kv8_ctas<2>(), C = 8 * p.nt;
     // lists: a warp a row from 1184 rows on (half the warps that fit), of short
     // lists from 592 on.  Measured (warp / CTA a row, us): 97 chunks, 1024 rows
     // 105 / 104, 2368 rows 169 / 218, 8000 rows 563 / 712; 25 chunks, 512 rows
     // 30 / 23, 1024 rows 33 / 42; 7 chunks, 512 rows 12 / 13
     p.warps = lists && (nq * hkv >= 4 * ctas || (nq * hkv >= 2 * ctas && max_chunks <= 32));
     if (p.warps) return p;
-    // a sequence's last group of columns may be a part
-    const int64_t rows = lists || one_each ? nq * hkv : hkv * (nq * G / (8 * p.nt) + n_seq);
-    if (max_chunks <= kv8_own_chunks(rows) && rows <= INT32_MAX) p.rows = rows;
+    // rows at most (a sequence's last group of columns may be a part), and with
+    // equally many new tokens a sequence
+    const bool each = lists || one_each;
+    const int64_t rows = each ? nq * hkv : hkv * ((nq * G + n_seq * (C - G)) / C);
+    const int64_t likely = each ? rows : std::min(rows, hkv * n_seq * ceil_div<int64_t>(ceil_div<int64_t>(nq, n_seq) * G, C));
+    for (int lg = 3; lg > 0 && p.cluster == 1; --lg)
+        if (max_chunks > 16 && max_chunks > 4 << lg && likely <= kv8_clusters(lg)) p.cluster = 1 << lg;
+    if (max_chunks <= p.cluster * kv8_cta_chunks(likely * p.cluster) && rows * p.cluster <= INT32_MAX) p.rows = rows;
     else p.ws = (size_t)ctas * 2 * (p.nt == 1 ? kv8_part_floats<1>() : kv8_part_floats<2>()) * sizeof(float);
     return p;
 }
@@ -1047,24 +1171,24 @@ static int64_t kv8_max_chunks(int64_t nq, int32_t page, int32_t max_pages, int32
     return some < all ? some : all;
 }
 
-// A kernel's dynamic shared memory limit, raised once a device.
-static void kv8_allow_smem(const void* kern, size_t bytes, std::atomic<uint64_t>& done) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return;
-    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-    if (done.load(std::memory_order_acquire) & bit) return;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess)
-        done.fetch_or(bit, std::memory_order_release);
-}
-
 template <int FMT, int NT, bool LIST, int WARPS>
-static lsa_status launch_kv8_ctas(const Kv8AttnArgs& a, int n, cudaStream_t st) {
+static lsa_status launch_kv8_ctas(const Kv8AttnArgs& a, int n, int cluster, cudaStream_t st) {
     constexpr size_t smem = (size_t)WARPS * kKv8Warp;
     static std::atomic<uint64_t> allowed{0};
     kv8_allow_smem((const void*)kv8_split_kernel<FMT, NT, LIST, WARPS>, smem, allowed);
     {
         KTime kt_("kv8_split_kernel", st);
-        kv8_split_kernel<FMT, NT, LIST, WARPS><<<n, 32 * WARPS, smem, st>>>(a, kKv8Least);
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(n * cluster);
+        cfg.blockDim = dim3(32 * WARPS);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = st;
+        cudaLaunchAttribute at{};
+        at.id = cudaLaunchAttributeClusterDimension;
+        at.val.clusterDim = {(unsigned)cluster, 1u, 1u};
+        cfg.attrs = &at;
+        cfg.numAttrs = cluster > 1;
+        cudaLaunchKernelEx(&cfg, kv8_split_kernel<FMT, NT, LIST, WARPS>, a, kKv8Least);
     }
     return check_launch("kv8_split_kernel");
 }
@@ -1074,12 +1198,12 @@ static lsa_status launch_kv8_split(Kv8AttnArgs a, const Kv8Plan& p, int64_t n_se
     if (p.rows > 0) {
         a.own = LIST || one_each ? 1 : 2;
         if constexpr (NT == 1)
-            if (p.rows <= num_sms()) return launch_kv8_ctas<FMT, 1, LIST, 16>(a, (int)p.rows, st);
-        return launch_kv8_ctas<FMT, NT, LIST, kKv8Warps>(a, (int)p.rows, st);
+            if (p.rows <= num_sms()) return launch_kv8_ctas<FMT, 1, LIST, 16>(a, (int)p.rows, p.cluster, st);
+        return launch_kv8_ctas<FMT, NT, LIST, kKv8Warps>(a, (int)p.rows, p.cluster, st);
     }
     const int n = kv8_ctas<NT>();
     lsa_status s;
-    if ((s = launch_kv8_ctas<FMT, NT, LIST, kKv8Warps>(a, n, st)) != LSA_OK) return s;
+    if ((s = launch_kv8_ctas<FMT, NT, LIST, kKv8Warps>(a, n, 1, st)) != LSA_OK) return s;
     // the join's own scan runs while the split kernel drains
     cudaLaunchConfig_t cfg{};
     // a row's pieces: about n over the rows; rows of up to 16 by whole columns

@@ -173,6 +173,10 @@ def test_write_reads_strided_rows(lsa):
     (64, 1, 4, [3, 2], [6, 2], 0, 0),          # more queries than tokens: the first see nothing
     (16, 8, 4, [20000], [1], 0, 0),
     (32, 1, 8, [70000, 1], [1, 1], 0, 0),
+    (64, 1, 8, [30000, 50], [5, 3], 0, 0),     # pieces of rows, 16 columns
+    (16, 2, 4, [40000, 3], [1, 1], 0, 0),
+    (64, 2, 4, [5000, 0, 700, 9], [6, 0, 4, 12], 4, 2000),   # clusters, 16 columns
+    (64, 8, 1, [3000, 600, 33], [1, 1, 1], 0, 0),            # clusters of four
 ])
 def test_attention_against_64_bits(lsa, fmt, page, hkv, G, lens, new, sinks, window):
     rng = np.random.default_rng(sum(lens) + page)
@@ -238,7 +242,10 @@ def random_lists(rng, nq, hkv, n_idx, lens, seq, pads=0.2):
     (64, 4, 2, [700, 600], 300, 1100),         # a warp a row, long lists
     (64, 4, 2, [700, 600], 160, 40),           # a warp a row, short lists
     (32, 8, 1, [700, 600], 100, 200),          # a CTA a row, more rows than SMs
-    (16, 2, 8, [900, 600], 60, 4200),          # pieces of rows
+    (16, 2, 8, [900, 600], 60, 4200),          # a CTA a row, as many rows as SMs
+    (16, 2, 8, [900, 600], 60, 5300),          # pieces of rows
+    (16, 1, 4, [900, 600], 2, 27000),          # pieces of few rows
+    (64, 2, 1, [900, 600], 35, 1000),          # clusters of two
 ])
 def test_lists_against_64_bits(lsa, fmt, page, hkv, G, lens, nq, n_idx):
     rng = np.random.default_rng(nq + n_idx)
@@ -365,17 +372,19 @@ def test_offsets_past_32_bits(lsa):
 
 # ------------------------------------------------- streams, graphs, errors
 
-def small_case(lsa, rng, fmt="e4m3", wide=True):
+def small_case(lsa, rng, fmt="e4m3", wide=2):
+    """wide: the rows that the call's shapes allow get a CTA each (0), a cluster
+    each (1), or are cut into pieces (2)."""
     lens, hkv, page = [300, 77, 5], 2, 32
     kv, table = filled(lsa, rng, lens, hkv, page, fmt)
-    if wide:                                     # the stream form: rows of more than 48 chunks are possible
-        t = np.full((3, 200), -1, np.int32)
+    if wide:
+        t = np.full((3, (0, 200, 900)[wide]), -1, np.int32)
         t[:, :table.shape[1]] = table
         table = t
-    return kv, i32(table), i32(lens), torch.from_numpy(random_lists(rng, 3, hkv, 1700 if wide else 90, lens, [0, 1, 2])).cuda()
+    return kv, i32(table), i32(lens), torch.from_numpy(random_lists(rng, 3, hkv, (90, 1700, 27000)[wide], lens, [0, 1, 2])).cuda()
 
 
-@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("wide", [0, 1, 2])
 def test_graphs_share_nothing(lsa, wide):
     """Two captured graphs of the same calls, replayed in turn on two streams
     and with an eager call between, each with inputs of its own."""
@@ -506,7 +515,7 @@ def test_bad_pages_and_ranges_are_reported(lsa):
         lsa.check_device_error()
 
     rng = np.random.default_rng(33)
-    kv, table, lens, idx = small_case(lsa, rng, wide=False)
+    kv, table, lens, idx = small_case(lsa, rng, wide=0)
     K, V, scale = host(kv)
     q, hq = bf16(rng.standard_normal((3, 8, 128)))
     for bad in (-1, kv.n_pages, 2 ** 31 - 1):

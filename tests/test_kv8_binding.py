@@ -115,7 +115,7 @@ def test_abi_refusals(L):
     assert L.lsa_kv8_attn_workspace_bytes(cache(), 3, 8, 1, 3, 4000, 4, 600) == 0
     assert attn(mp=4000, nws=need - 1) == LSA_ENOSPACE and attn(mp=4000, ws=None) == LSA_ENOSPACE
 
-    def lists(Q=f, nq=3, hq=8, seq=None, n_seq=3, idx=f, n_idx=5000, ws=f, nws=1 << 30):
+    def lists(Q=f, nq=3, hq=8, seq=None, n_seq=3, idx=f, n_idx=40000, ws=f, nws=1 << 30):
         return L.lsa_kv8_sparse_attn(cache(), Q, 8 * 128, nq, hq, seq, f, f, n_seq, 4, idx, n_idx, f, f, ws, nws, None)
 
     for kw in (dict(Q=None), dict(idx=None), dict(n_idx=-1), dict(nq=4), dict(nq=-1), dict(n_seq=0, seq=f)):
