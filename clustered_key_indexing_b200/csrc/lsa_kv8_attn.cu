@@ -658,8 +658,8 @@ __global__ void __launch_bounds__(32 * kKv8ListWarps, 2) kv8_list_kernel(Kv8Attn
 // memory: no second kernel, no workspace.  8 rows of 282 chunks (9000 tokens):
 // 11.6 us, 16.7 in the stream (captured; called one by one 14.4 and 24.2).
 //
-// Bound by HBM: a million tokens of 8 kv-heads (2.15 GB) in 330 to 375 us, 32
-// sequences of 2K to 32K tokens (1.21 GB) in 205 us, 5.9 TB/s; the warps of a
+// Bound by HBM: a million tokens of 8 kv-heads (2.15 GB) in 333 to 345 us, 32
+// sequences of 2K to 32K tokens (1.21 GB) in 191 us, 6.3 TB/s; the warps of a
 // CTA take neighbouring chunks, so that it reads whole pages at a time.
 struct Kv8Seq {
     int64_t base;     // first chunk of the sequence in the stream
@@ -700,31 +700,47 @@ __device__ __forceinline__ void kv8_seq(const Kv8AttnArgs& a, int64_t b, Kv8Seq&
     }
 }
 
-// A sequence's share of a stream: its chunks, or (ROWS) its rows.
+// What a row costs a CTA of the stream beside its chunks, in chunks: its last
+// warp is waited for, its sums are joined, the next one's copies begin.  It
+// counts in the shares where they are long enough (kKv8Padded chunks a CTA), or
+// CTAs with many short rows would come last (64 sequences of 480 to 8000 tokens
+// 98 us, 124 without; 8 and 32 in place of 16 104 and 99).
+constexpr int kKv8RowCost = 16, kKv8Padded = 64;
+
+// A sequence's share of a stream: its chunks and its rows' cost, or (ROWS) its rows.
 template <int NT, bool LIST, int WARPS = kKv8Warps, bool ROWS = false>
 struct Kv8Scan {
     int64_t total, per;
+    int pad;                        // what a row counts beside its chunks
     long long begin, count, round;  // this thread's sequence in the CTA's first round: its place, its share; the round's
 
     __device__ __forceinline__ long long share_of(const Kv8AttnArgs& a, int64_t b) const {
         if (b >= a.n_seq) return 0;
         Kv8Seq q;
         kv8_seq<NT, LIST>(a, b, q);
-        return ROWS ? q.rows : (int64_t)q.chunks * q.rows;
+        return ROWS ? q.rows : (int64_t)(q.chunks + pad) * q.rows;
+    }
+    __device__ __forceinline__ void sum(const Kv8AttnArgs& a) {
+        count = share_of(a, threadIdx.x);
+        begin = kv8_block_scan<WARPS>(count, round);
+        total = round;
+        for (int64_t b0 = 32 * WARPS; b0 < a.n_seq; b0 += 32 * WARPS) {
+            long long all;
+            kv8_block_scan<WARPS>(share_of(a, b0 + threadIdx.x), all);
+            total += all;
+        }
     }
     // The stream's length and each CTA's share of it (`least`: a CTA takes at
     // least so much).
     __device__ __forceinline__ void init(const Kv8AttnArgs& a, int n_cta, int least) {
+        pad = 0;
         if constexpr (LIST) {
             total = a.nq * a.hkv * (int64_t)max(1, (a.n_idx + 31) / 32);
         } else {
-            count = share_of(a, threadIdx.x);
-            begin = kv8_block_scan<WARPS>(count, round);
-            total = round;
-            for (int64_t b0 = 32 * WARPS; b0 < a.n_seq; b0 += 32 * WARPS) {
-                long long all;
-                kv8_block_scan<WARPS>(share_of(a, b0 + threadIdx.x), all);
-                total += all;
+            sum(a);
+            if (!ROWS && total >= (int64_t)kKv8Padded * n_cta) {
+                pad = kKv8RowCost;
+                sum(a);
             }
         }
         // `least` a CTA, but no more than the rows have on average: short rows
@@ -839,6 +855,7 @@ __global__ void __launch_bounds__(32 * WARPS, NT == 1 && WARPS == 8 ? 2 : 1) kv8
     Kv8Seq q;
     int64_t b, w0 = 0, w1 = 0;
     int r = 0, t0 = 0, n = 0;  // row of the sequence, its first chunk here, how many
+    int pad = 0;
     if (own) {
         const int item = (int)(blockIdx.x / csize);
         if (LIST || a.own == 1) {
@@ -864,18 +881,25 @@ __global__ void __launch_bounds__(32 * WARPS, NT == 1 && WARPS == 8 ? 2 : 1) kv8
         w1 = min(scan.total, w0 + scan.per);
         if (w0 >= w1) return;
         b = scan.find(a, w0, q);
+        pad = scan.pad;
     }
     for (int64_t w = w0;;) {
+        bool whole = true, begins = true;  // the piece is the whole row, begins it
         if (!own) {
-            while (w >= q.base + (int64_t)q.chunks * q.rows) {  // the next sequence that has rows
-                const int64_t next = q.base + (int64_t)q.chunks * q.rows;
+            while (w >= q.base + (int64_t)(q.chunks + pad) * q.rows) {  // the next sequence that has rows
+                const int64_t next = q.base + (int64_t)(q.chunks + pad) * q.rows;
                 kv8_seq<NT, LIST>(a, ++b, q);
                 q.base = next;
             }
+            const int units = q.chunks + pad;
             const int64_t rel = w - q.base;
-            r = rel >> 31 ? (int)(rel / q.chunks) : (int)((uint32_t)rel / (uint32_t)q.chunks);
-            t0 = (int)(rel - (int64_t)r * q.chunks);
-            n = (int)min((int64_t)(q.chunks - t0), w1 - w);
+            r = rel >> 31 ? (int)(rel / units) : (int)((uint32_t)rel / (uint32_t)units);
+            const int u0 = (int)(rel - (int64_t)r * units), nu = (int)min((int64_t)(units - u0), w1 - w);
+            begins = u0 == 0;
+            whole = nu == units;
+            t0 = max(0, u0 - pad);
+            n = max(0, u0 + nu - pad) - t0;
+            w += nu;
         }
         const int g = r / q.groups, cg = r % q.groups;
         const int ta = t0 + wid, tb = t0 + n;  // neighbouring chunks at the same time: whole pages of DRAM
@@ -938,8 +962,7 @@ __global__ void __launch_bounds__(32 * WARPS, NT == 1 && WARPS == 8 ? 2 : 1) kv8
             }
         }
         __syncthreads();
-        const bool final_ = n == q.chunks;
-        float* part = a.part + ((int64_t)blockIdx.x * 2 + (t0 == 0 ? 1 : 0)) * kv8_part_floats<NT>();
+        float* part = a.part + ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * kv8_part_floats<NT>();
         for (int e = tid; e < 8 * NT * kD / 4; e += 32 * WARPS) {  // four sums of a column
             const int c = e / (kD / 4), dim = e % (kD / 4) * 4;
             const int64_t orow = kv8_out_row<NT>(a, q, cg, g, c);
@@ -960,7 +983,7 @@ __global__ void __launch_bounds__(32 * WARPS, NT == 1 && WARPS == 8 ? 2 : 1) kv8
             if (CLUSTER && csize > 1) {
                 *reinterpret_cast<float4*>(sc(c) + dim * 4) = acc;
                 if (dim == 0) *reinterpret_cast<float2*>(cml + 2 * c) = make_float2(M, l);
-            } else if (final_) {
+            } else if (whole) {
                 kv8_store(a, orow, dim, acc, M, l);
             } else {
                 *reinterpret_cast<float4*>(part + c * kD + dim) = acc;
@@ -989,7 +1012,6 @@ __global__ void __launch_bounds__(32 * WARPS, NT == 1 && WARPS == 8 ? 2 : 1) kv8
             cluster_barrier();  // nobody leaves while others read its sums
             return;
         }
-        w += n;
         if (own || w >= w1) return;
         __syncthreads();
     }
@@ -1031,9 +1053,10 @@ __global__ void __launch_bounds__(32 * kKv8Warps) kv8_join_kernel(Kv8AttnArgs a,
     if (w1 < scan.total) scan.find(a, w1, q);
     asm volatile("griddepcontrol.wait;\n" ::: "memory");  // before any exit: this grid's end is the call's end
     if (w1 >= scan.total) return;
+    const int units = q.chunks + scan.pad;
     const int64_t rel = w1 - q.base;
-    const int r = rel >> 31 ? (int)(rel / q.chunks) : (int)((uint32_t)rel / (uint32_t)q.chunks);
-    const int64_t begin = q.base + (int64_t)r * q.chunks, end = begin + q.chunks;
+    const int r = rel >> 31 ? (int)(rel / units) : (int)((uint32_t)rel / (uint32_t)units);
+    const int64_t begin = q.base + (int64_t)r * units, end = begin + units;
     if (begin == w1 || begin < w0) return;
     const int n = (int)((end - 1) / scan.per - c) + 1;
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, cg = r % q.groups, g = r / q.groups;
@@ -1122,10 +1145,14 @@ static int kv8_clusters(int lg) {
 // Chunks a CTA may have of a row that is not in the stream, where `ctas` of them
 // run: a CTA takes 4.5 us and 2 us for a chunk of each of its 16 warps; the
 // stream 13 us, and then the same on all SMs (its shares are equal, so the cap
-// is for rows of unequal lengths).  More CTAs than SMs: 128.
+// is for rows of unequal lengths).  More CTAs than SMs, two of 8 warps an SM: 128
+// where they nearly fill the GPU once (own / stream, us: 256 rows of 125 chunks
+// 48 / 54, of unequal lengths up to that 43 / 48), else 64 (384 rows of 125
+// 82 / 73, 60 / 49; of 63 46 / 45, 36 / 47; 1024 rows of 94 131 / 141, 87 / 83).
 static int64_t kv8_cta_chunks(int64_t ctas) {
     const int64_t n = num_sms();
-    return ctas > n ? 128 : std::min<int64_t>(160, 720 * n / (10 * n - 9 * ctas));
+    if (ctas > n) return 4 * ctas >= 5 * n && ctas <= 2 * n ? 128 : 64;
+    return std::min<int64_t>(160, 720 * n / (10 * n - 9 * ctas));
 }
 
 // How a call's rows meet the GPU: one warp a row (lists only), one CTA or

@@ -177,6 +177,8 @@ def test_write_reads_strided_rows(lsa):
     (16, 2, 4, [40000, 3], [1, 1], 0, 0),
     (64, 2, 4, [5000, 0, 700, 9], [6, 0, 4, 12], 4, 2000),   # clusters, 16 columns
     (64, 8, 1, [3000, 600, 33], [1, 1, 1], 0, 0),            # clusters of four
+    (64, 8, 1, [60000, 17000, 300, 0, 7], [1, 1, 1, 1, 1], 0, 0),   # pieces long enough that short rows count more
+    (32, 8, 4, [24000, 17000, 300, 9], [4, 8, 3, 1], 0, 0),
 ])
 def test_attention_against_64_bits(lsa, fmt, page, hkv, G, lens, new, sinks, window):
     rng = np.random.default_rng(sum(lens) + page)
