@@ -1,5 +1,9 @@
 """The paged 8-bit K/V cache on the GPU, through the binding, against the
 same operators written out in 64 bits (kv8_ref)."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -455,6 +459,36 @@ def test_a_captured_decode_step(lsa):
         start += 1
         lens += 1
     lsa.check_device_error()
+
+
+def test_first_calls_inside_a_capture():
+    """A process whose first calls are captured: what the library asks the
+    device for once is allowed there."""
+    code = """
+import torch, clustered_key_indexing_b200 as lsa
+i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+kv = lsa.KV8(400, 2, page=64)
+table = torch.arange(400, dtype=torch.int32, device="cuda")[None]
+wide = torch.cat([table] * 8, 1)
+k, q = torch.randn(1, 2, 128, device="cuda").bfloat16(), torch.randn(1, 8, 128, device="cuda").bfloat16()
+idx, lens, start, pages = torch.randint(0, 19000, (1, 2, 3000), dtype=torch.int32, device="cuda"), i32([20000]), i32([19999]), ([1, 2], [350, 351])
+def calls():
+    lsa.kv8_write(kv, k, k, table, start)
+    lsa.kv8_copy_pages(kv, *pages)
+    return lsa.kv8_attn(q, kv, table, lens) + lsa.kv8_attn(q, kv, wide, lens) + lsa.kv8_sparse_attn(q, kv, table, lens, idx)
+g = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(g):
+    out = calls()
+g.replay()
+want = calls()
+torch.cuda.synchronize()
+assert all(torch.equal(x, y) for x, y in zip(out, want)) and out[0].abs().max() >= 0
+lsa.check_device_error()
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0, r.stderr
 
 
 def test_another_stream(lsa):
