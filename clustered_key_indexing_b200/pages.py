@@ -228,6 +228,7 @@ class KV8Pages:
 
     def advance(self, sids, counts=None):
         """Count tokens that were written into reserved pages."""
+        sids = list(sids)
         seqs, counts = self._counts("advance", sids, counts)
         for sid, seq, c in zip(sids, seqs, counts):
             if seq.len + c > len(seq.pages) * self.kv.page:

@@ -201,3 +201,13 @@ def test_reserve_and_advance():
     with pytest.raises(LSAError):
         p.reserve([a], [200])
     assert len(p.pages(a)) == 3 and p.used_pages == 4
+
+
+def test_sequences_may_come_from_a_generator():
+    p = KV8Pages(pool(4), HostOps())
+    a, b = p.add(), p.add()
+    p.reserve((s for s in (a, b)), [3, 20])
+    with pytest.raises(ValueError, match="advance"):
+        p.advance((s for s in (a, b)), [3, 40])
+    p.advance((s for s in (a, b)), [3, 20])
+    assert (p.len(a), p.len(b)) == (3, 20) and p.used_pages == 3
