@@ -3,7 +3,7 @@ and the appends, forks, truncations and moves that keep it so.
 
 Host logic only; the codes are written by lsa_kv8_write and moved by
 lsa_kv8_copy_pages.  A page belongs to every sequence whose table names it
-(a reference count); a fork shares all pages of its parent, and the first
+(a reference count); a fork shares the pages of its parent's tokens, and the first
 append of either into a shared page that is still open copies it first.
 Free pages are handed out lowest number first, so that `compact` has little
 to move.  The calls are taken from an `ops` object, as in `seqshard`, so that
@@ -114,10 +114,11 @@ class KV8Pages:
     def fork(self, sid) -> int:
         """A sequence with the same tokens, sharing their pages."""
         parent = self._seq(sid)
-        for p in parent.pages:
+        pages = parent.pages[:-(-parent.len // self.kv.page)]  # what it reserved stays its own
+        for p in pages:
             self.refs[p] += 1
         new = self.add()
-        self._seqs[new] = _Sequence(list(parent.pages), parent.len)
+        self._seqs[new] = _Sequence(pages, parent.len)
         return new
 
     def free(self, sid):

@@ -204,10 +204,26 @@ def test_reserve_and_advance():
 
 
 def test_sequences_may_come_from_a_generator():
-    p = KV8Pages(pool(4), HostOps())
+    p = pool(4)
     a, b = p.add(), p.add()
     p.reserve((s for s in (a, b)), [3, 20])
     with pytest.raises(ValueError, match="advance"):
         p.advance((s for s in (a, b)), [3, 40])
     p.advance((s for s in (a, b)), [3, 20])
     assert (p.len(a), p.len(b)) == (3, 20) and p.used_pages == 3
+
+
+@pytest.mark.parametrize("held", [16, 20])
+def test_a_fork_does_not_share_reserved_pages(held):
+    rng = np.random.default_rng(7)
+    p = pool(8)
+    a = p.add()
+    p.append([a], rows(rng, held), rows(rng, held), [held])
+    p.reserve([a], [20])
+    b = p.fork(a)
+    for s in (a, b):
+        p.append([s], rows(rng, 20), rows(rng, 20), [20])
+    assert not set(p.pages(a)[1:]) & set(p.pages(b)[1:])
+    p.free(a)
+    p.free(b)
+    assert p.free_pages == 8
