@@ -602,11 +602,12 @@ struct Kv8Walk {
 // Many rows: one warp per (query, kv-head), kv-head major so that the warps
 // resident at one time read one head's rows, which keeps them in L2.  A step
 // is about 240 instructions, 115 of them integer and conversion (64 turn codes
-// into fp16, two cycles each): 61% of that pipe's cycles and 63% of the issue
-// slots are used, the tensor pipe a third.  1000 rows x 8 kv-heads of 3076
-// entries: 570 us, 11.2 TB/s from L2 (bf16 rows of the same keys are twice the
-// bytes).  Two steps interleaved with 12 warps an SM took 686 us instead of
-// 603, one CTA of fewer warps and more registers 960.
+// into fp16, two cycles each): 60% of that pipe's cycles, 62% of the issue slots
+// and 61% of the L1 data pipe are used, the tensor pipe a third; the copies alone
+// take 324 us of the 570.  1000 rows x 8 kv-heads of 3076 entries: 570 us, 11.2
+// TB/s from L2 (bf16 rows of the same keys are twice the bytes; int8 codes, five
+// instructions for four values instead of two, 708).  Two steps interleaved with
+// 12 warps an SM took 686 us instead of 603, 20 warps of 96 registers 684.
 template <int FMT>
 __global__ void __launch_bounds__(32 * kKv8ListWarps, 2) kv8_list_kernel(Kv8AttnArgs a) {
     const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
