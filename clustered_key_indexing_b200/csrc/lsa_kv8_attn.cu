@@ -38,7 +38,8 @@
 namespace lsa {
 
 constexpr int kKv8ListWarps = 8;
-constexpr float kKv8Head = 12.f;   // log2 of P's headroom
+constexpr int kKv8Head = 12;       // log2 of P's headroom: P is at most 2^(12 + 2), fp16 ends at 65504
+constexpr float kKv8Unit = 1.f / (1 << kKv8Head);
 constexpr float kKv8Lazy = 2.f;    // log2 growth that moves the running maximum
 
 struct Kv8AttnArgs {
@@ -218,7 +219,7 @@ __device__ __forceinline__ void kv8_softmax(Kv8State<NT>& s, const float (&sc)[N
     bool grew = fmaxf(vs0, vs1) > s.vref;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
-        grew = grew || fmaxf(sc[nt][0], sc[nt][2]) > s.m[nt][0] + kKv8Lazy || fmaxf(sc[nt][1], sc[nt][3]) > s.m[nt][1] + kKv8Lazy;
+        grew = grew || fmaxf(sc[nt][0], sc[nt][2]) - s.m[nt][0] > kKv8Lazy || fmaxf(sc[nt][1], sc[nt][3]) - s.m[nt][1] > kKv8Lazy;
     if (__any_sync(0xffffffffu, grew)) {
         // the step's largest V scale: positive floats order as integers
         const float vmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(vs0, vs1))));
@@ -245,13 +246,14 @@ __device__ __forceinline__ void kv8_softmax(Kv8State<NT>& s, const float (&sc)[N
             }
         }
     }
-    // 1 / vref: the reciprocal of a power of two, exactly
-    const float iv = __uint_as_float(0x7F000000u - __float_as_uint(s.vref)), w0 = vs0 * iv, w1 = vs1 * iv;
+    // 2^12 / vref: a power of two, exactly.  The headroom goes here and not into the
+    // maximum: at scores of 2^25 and more a float's spacing would round m - 12, and
+    // its error be a factor of P.  The differences sc - m are exact next to m.
+    const float iv = __uint_as_float(0x7F000000u + (kKv8Head << 23) - __float_as_uint(s.vref)), w0 = vs0 * iv, w1 = vs1 * iv;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        const float b0 = s.m[nt][0] - kKv8Head, b1 = s.m[nt][1] - kKv8Head;
-        const float e0 = ex2(sc[nt][0] - b0), e1 = ex2(sc[nt][1] - b1);
-        const float e2 = ex2(sc[nt][2] - b0), e3 = ex2(sc[nt][3] - b1);
+        const float e0 = ex2(sc[nt][0] - s.m[nt][0]), e1 = ex2(sc[nt][1] - s.m[nt][1]);
+        const float e2 = ex2(sc[nt][2] - s.m[nt][0]), e3 = ex2(sc[nt][3] - s.m[nt][1]);
         s.l[nt][0] += e0 + e2;
         s.l[nt][1] += e1 + e3;
         pb[nt][0] = movmatrix_t(pack_f16x2(e0 * w0, e1 * w0));
@@ -630,14 +632,14 @@ __global__ void __launch_bounds__(32 * kKv8ListWarps, 2) kv8_list_kernel(Kv8Attn
     uint16_t* os = reinterpret_cast<uint16_t*>(lsm + (threadIdx.x >> 5) * kKv8Warp);
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-        const float l = s.l[0][c], f = l > 0.f || l != l ? s.vref / l : 0.f;
+        const float l = s.l[0][c], f = l > 0.f || l != l ? s.vref * kKv8Unit / l : 0.f;
 #pragma unroll
         for (int mt = 0; mt < 8; ++mt) {
             os[(2 * tq + c) * kD + 16 * mt + gq] = bf16_bits(s.o[0][mt][c] * f);
             os[(2 * tq + c) * kD + 16 * mt + gq + 8] = bf16_bits(s.o[0][mt][2 + c] * f);
         }
         if (a.lse && gq == 0 && 2 * tq + c < a.G)
-            a.lse[q * hq + g * a.G + 2 * tq + c] = l > 0.f || l != l ? s.m[0][c] - kKv8Head + log2f(l) : -CUDART_INF_F;
+            a.lse[q * hq + g * a.G + 2 * tq + c] = l > 0.f || l != l ? s.m[0][c] + log2f(l) : -CUDART_INF_F;
     }
     __syncwarp();
     uint4* orow = reinterpret_cast<uint4*>(a.O + (q * hq + g * a.G) * kD);
@@ -797,7 +799,7 @@ __device__ __forceinline__ void kv8_store(const Kv8AttnArgs& a, int64_t orow, in
     const bool any = l > 0.f || l != l;
     const float f = any ? 1.f / l : 0.f;
     *reinterpret_cast<uint2*>(a.O + orow * kD + d) = make_uint2(pack_bf16x2(x.x * f, x.y * f), pack_bf16x2(x.z * f, x.w * f));
-    if (d == 0 && a.lse) a.lse[orow] = any ? m - kKv8Head + log2f(l) : -CUDART_INF_F;
+    if (d == 0 && a.lse) a.lse[orow] = any ? m + log2f(l) : -CUDART_INF_F;
 }
 
 // Number of this CTA in its cluster, CTAs of the cluster, the cluster's barrier
@@ -951,8 +953,8 @@ __global__ void __launch_bounds__(32 * WARPS, NT == 1 && WARPS == 8 ? 2 : 1) kv8
                     float* p = so(wid) + (8 * nt + 2 * tq + c) * kKv8Pad + gq;
 #pragma unroll
                     for (int mt = 0; mt < 8; ++mt) {
-                        p[16 * mt] = s.o[nt][mt][c] * s.vref;
-                        p[16 * mt + 8] = s.o[nt][mt][2 + c] * s.vref;
+                        p[16 * mt] = s.o[nt][mt][c] * (s.vref * kKv8Unit);
+                        p[16 * mt + 8] = s.o[nt][mt][2 + c] * (s.vref * kKv8Unit);
                     }
                     if (gq == 0) { sml[2 * col] = s.m[nt][c]; sml[2 * col + 1] = s.l[nt][c]; }
                 }
