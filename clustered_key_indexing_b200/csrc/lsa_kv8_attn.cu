@@ -794,13 +794,22 @@ __device__ __forceinline__ int64_t kv8_out_row(const Kv8AttnArgs& a, const Kv8Se
     return (q.q0 + (cc >> a.lgG)) * (a.G * a.hkv) + g * a.G + (cc & (a.G - 1));
 }
 
-// Four sums of one output row (dims d .. d + 3).
-__device__ __forceinline__ void kv8_store(const Kv8AttnArgs& a, int64_t orow, int d, float4 x, float m, float l) {
-    const bool any = l > 0.f || l != l;
-    const float f = any ? 1.f / l : 0.f;
-    *reinterpret_cast<uint2*>(a.O + orow * kD + d) = make_uint2(pack_bf16x2(x.x * f, x.y * f), pack_bf16x2(x.z * f, x.w * f));
-    if (d == 0 && a.lse) a.lse[orow] = any ? m + log2f(l) : -CUDART_INF_F;
+// Partial states are kept as (m, l) and the output that their keys alone would
+// give: it is within V's range, which sums that are yet to be divided leave.
+// f / l, 0 for a state without a key (a NaN stays).
+__device__ __forceinline__ float kv8_over(float f, float l) { return l > 0.f || l != l ? f / l : 0.f; }
+
+__device__ __forceinline__ void kv8_add(float4& acc, const float4& x, float f) {
+    acc = make_float4(acc.x + x.x * f, acc.y + x.y * f, acc.z + x.z * f, acc.w + x.w * f);
 }
+
+// Four elements of one output row (dims d .. d + 3).
+__device__ __forceinline__ void kv8_store(const Kv8AttnArgs& a, int64_t orow, int d, float4 x, float m, float l) {
+    *reinterpret_cast<uint2*>(a.O + orow * kD + d) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+    if (d == 0 && a.lse) a.lse[orow] = l > 0.f || l != l ? m + log2f(l) : -CUDART_INF_F;
+}
+
+constexpr int kKv8Cluster = 8;  // CTAs of a cluster at most
 
 // Number of this CTA in its cluster, CTAs of the cluster, the cluster's barrier
 // (which orders shared memory), and a load from CTA `rank`'s shared memory.
@@ -951,10 +960,11 @@ __global__ void __launch_bounds__(32 * WARPS, NT == 1 && WARPS == 8 ? 2 : 1) kv8
                 for (int c = 0; c < 2; ++c) {
                     const int col = wid * 8 * NT + 8 * nt + 2 * tq + c;
                     float* p = so(wid) + (8 * nt + 2 * tq + c) * kKv8Pad + gq;
+                    const float f = kv8_over(s.vref * kKv8Unit, s.l[nt][c]);
 #pragma unroll
                     for (int mt = 0; mt < 8; ++mt) {
-                        p[16 * mt] = s.o[nt][mt][c] * (s.vref * kKv8Unit);
-                        p[16 * mt + 8] = s.o[nt][mt][2 + c] * (s.vref * kKv8Unit);
+                        p[16 * mt] = s.o[nt][mt][c] * f;
+                        p[16 * mt + 8] = s.o[nt][mt][2 + c] * f;
                     }
                     if (gq == 0) { sml[2 * col] = s.m[nt][c]; sml[2 * col + 1] = s.l[nt][c]; }
                 }
@@ -970,19 +980,20 @@ __global__ void __launch_bounds__(32 * WARPS, NT == 1 && WARPS == 8 ? 2 : 1) kv8
             const int c = e / (kD / 4), dim = e % (kD / 4) * 4;
             const int64_t orow = kv8_out_row<NT>(a, q, cg, g, c);
             if (orow < 0) continue;
-            float M = -FLT_MAX, l = 0.f;
+            float M = -FLT_MAX, l = 0.f, weight[WARPS];
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < WARPS; ++i) M = fmaxf(M, sml[2 * (i * 8 * NT + c)]);
 #pragma unroll
             for (int i = 0; i < WARPS; ++i) {
                 const float2 ml = *reinterpret_cast<const float2*>(sml + 2 * (i * 8 * NT + c));
-                if (ml.y == -1.f) continue;
-                const float f = ex2(ml.x - M);
-                const float4 x = *reinterpret_cast<const float4*>(so(i) + c * kKv8Pad + dim);
-                l += ml.y * f;
-                acc = make_float4(acc.x + x.x * f, acc.y + x.y * f, acc.z + x.z * f, acc.w + x.w * f);
+                weight[i] = ml.y == -1.f ? 0.f : ml.y * ex2(ml.x - M);
+                l += weight[i];
             }
+            const float f = kv8_over(1.f, l);
+#pragma unroll
+            for (int i = 0; i < WARPS; ++i)  // a warp without a chunk has written no sums
+                if (weight[i] != 0.f) kv8_add(acc, *reinterpret_cast<const float4*>(so(i) + c * kKv8Pad + dim), weight[i] * f);
             if (CLUSTER && csize > 1) {
                 *reinterpret_cast<float4*>(sc(c) + dim * 4) = acc;
                 if (dim == 0) *reinterpret_cast<float2*>(cml + 2 * c) = make_float2(M, l);
@@ -999,17 +1010,29 @@ __global__ void __launch_bounds__(32 * WARPS, NT == 1 && WARPS == 8 ? 2 : 1) kv8
                 const int c = e / (kD / 4), dim = e % (kD / 4) * 4;
                 const int64_t orow = kv8_out_row<NT>(a, q, cg, g, c);
                 if (orow < 0) continue;
+                const uint32_t pm = smem_u32(cml + 2 * c), ps = smem_u32(sc(c) + dim * 4);
+                float2 ml[kKv8Cluster];
+                float4 x[kKv8Cluster];
                 float M = -FLT_MAX, l = 0.f;
                 float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                const uint32_t pm = smem_u32(cml + 2 * c), ps = smem_u32(sc(c) + dim * 4);
-                for (int i = 0; i < csize; ++i) {
-                    const float2 ml = peer_f2(peer_smem(pm, i));
-                    const float4 x = peer_f4(peer_smem(ps, i));
-                    const float m = fmaxf(M, ml.x), fa = ex2(M - m), fb = ex2(ml.x - m);
-                    acc = make_float4(acc.x * fa + x.x * fb, acc.y * fa + x.y * fb, acc.z * fa + x.z * fb, acc.w * fa + x.w * fb);
-                    l = l * fa + ml.y * fb;
-                    M = m;
+#pragma unroll
+                for (int i = 0; i < kKv8Cluster; ++i) {
+                    ml[i] = make_float2(-FLT_MAX, 0.f);
+                    x[i] = acc;
+                    if (i < csize) {
+                        ml[i] = peer_f2(peer_smem(pm, i));
+                        x[i] = peer_f4(peer_smem(ps, i));
+                    }
+                    M = fmaxf(M, ml[i].x);
                 }
+#pragma unroll
+                for (int i = 0; i < kKv8Cluster; ++i) {
+                    ml[i].y *= ex2(ml[i].x - M);
+                    l += ml[i].y;
+                }
+                const float f = kv8_over(1.f, l);
+#pragma unroll
+                for (int i = 0; i < kKv8Cluster; ++i) kv8_add(acc, x[i], ml[i].y * f);
                 kv8_store(a, orow, dim, acc, M, l);
             }
             cluster_barrier();  // nobody leaves while others read its sums
@@ -1020,26 +1043,32 @@ __global__ void __launch_bounds__(32 * WARPS, NT == 1 && WARPS == 8 ? 2 : 1) kv8
     }
 }
 
-// One column of n partial states, a lane four of its sums: states i0, i0 + di,
-// ... of which the first is CTA c's slot 1 and the others the slots 0 of the
-// CTAs after it.
+// One column of n partial states, of which the first is CTA c's slot 1 and the
+// others the slots 0 of the CTAs after it: (M, l) of all of them, and a lane's
+// four elements of the states i0, i0 + di, ... weighted by their share of l.
 template <int NT>
 __device__ __forceinline__ float4 kv8_join_column(const Kv8AttnArgs& a, int64_t c, int col, int i0, int di, int n, float& M,
                                                   float& l) {
-    constexpr int kPart = kv8_part_floats<NT>();
     const int lane = threadIdx.x & 31;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto state = [&](int i) { return a.part + (2 * (c + i) + (i == 0)) * kv8_part_floats<NT>(); };
+    auto ml_of = [&](int i) { return *reinterpret_cast<const float2*>(state(i) + 8 * NT * kD + 2 * col); };
     M = -FLT_MAX;
     l = 0.f;
+    for (int i = lane; i < n; i += 32) M = fmaxf(M, ml_of(i).x);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    for (int i = lane; i < n; i += 32) {
+        const float2 ml = ml_of(i);
+        l += ml.y * ex2(ml.x - M);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+    const float f = kv8_over(1.f, l);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int i = i0; i < n; i += di) {
-        const float* p = a.part + (2 * (c + i) + (i == 0)) * kPart;
-        const float2 ml = *reinterpret_cast<const float2*>(p + 8 * NT * kD + 2 * col);
-        const float4 x = *reinterpret_cast<const float4*>(p + col * kD + 4 * lane);
-        const float m = fmaxf(M, ml.x), fa = ex2(M - m), fb = ex2(ml.x - m);
-        acc = make_float4(acc.x * fa + x.x * fb, acc.y * fa + x.y * fb, acc.z * fa + x.z * fb, acc.w * fa + x.w * fb);
-        l = l * fa + ml.y * fb;
-        M = m;
+        const float2 ml = ml_of(i);
+        kv8_add(acc, *reinterpret_cast<const float4*>(state(i) + col * kD + 4 * lane), ml.y * ex2(ml.x - M) * f);
     }
     return acc;
 }
@@ -1076,23 +1105,13 @@ __global__ void __launch_bounds__(32 * kKv8Warps) kv8_join_kernel(Kv8AttnArgs a,
     const int64_t orow = kv8_out_row<NT>(a, q, cg, g, blockIdx.y);
     if (orow < 0) return;
     __shared__ float4 s_acc[kKv8Warps][32];
-    __shared__ float2 s_ml[kKv8Warps];
     float M, l;
     s_acc[wid][lane] = kv8_join_column<NT>(a, c, blockIdx.y, wid, kKv8Warps, n, M, l);
-    if (lane == 0) s_ml[wid] = make_float2(M, l);
     __syncthreads();
     if (wid > 0) return;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-    l = 0.f;
 #pragma unroll
-    for (int i = 0; i < kKv8Warps; ++i) M = fmaxf(M, s_ml[i].x);
-#pragma unroll
-    for (int i = 0; i < kKv8Warps; ++i) {
-        const float f = ex2(s_ml[i].x - M);
-        const float4 x = s_acc[i][lane];
-        l += s_ml[i].y * f;
-        sum = make_float4(sum.x + x.x * f, sum.y + x.y * f, sum.z + x.z * f, sum.w + x.w * f);
-    }
+    for (int i = 0; i < kKv8Warps; ++i) kv8_add(sum, s_acc[i][lane], 1.f);
     kv8_store(a, orow, 4 * lane, sum, M, l);
 }
 

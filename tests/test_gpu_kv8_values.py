@@ -1,0 +1,53 @@
+"""Attention over the 8-bit cache where the values' magnitudes are large or
+tiny."""
+import numpy as np
+import pytest
+import torch
+
+import kv8_ref as ref
+from kv8_forms import FORMS, attend, bf16, check, one_sequence, values
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def lsa():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import clustered_key_indexing_b200 as m
+    m.check_device_error()
+    return m
+
+
+def attended(q, k, v, vs, fmt):
+    """kv8_ref.attend with the values' share of the bound taken from what is
+    attended: a probability's absolute rounding is 2^-25 where the largest
+    product of a probability and a V scale is held as 2^12 or more, so a key
+    adds 2^-37 of that product times the largest code, over l."""
+    o, lse, tol, tl = ref.attend(q, k, v, 0.0)
+    x = q @ k.T / np.sqrt(128)
+    p = np.exp(x - x.max(1, keepdims=True))
+    return o, lse, tol + (k.shape[0] * 2.0 ** -37 * ref.QMAX[fmt] * (p * vs).max(1) / p.sum(1))[:, None], tl
+
+
+def compare(lsa, form, kv, table, n, q, hq, fmt):
+    o, lse, keys = attend(lsa, form, q, kv, table, n)
+    G = q.shape[1]
+    k, v, vs = values(kv, table, fmt, 0)
+    for i, j in enumerate(keys):
+        want, wl, tol, tl = attended(hq[i], k[j], v[j], vs[j], fmt)
+        for h in range(G):
+            check(o[i, h], want[h], tol[h])
+        check(lse[i], wl, tl)
+    lsa.check_device_error()
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("fmt,e", [("e4m3", 126), ("int8", 118), ("e4m3", -90), ("int8", 100)])
+def test_values_of_any_magnitude(lsa, fmt, e, form):
+    rng = np.random.default_rng(170 + e)
+    n, nq, G = 1500, 16, 4
+    v = np.clip(rng.standard_normal((n, 1, 128)) + 0.5, -1.9, 1.9) * 2.0 ** e
+    kv, table = one_sequence(lsa, rng.standard_normal((n, 1, 128)), v, 32, fmt)
+    q, hq = bf16(rng.standard_normal((nq, G, 128)))
+    compare(lsa, form, kv, table, n, q, hq, fmt)
