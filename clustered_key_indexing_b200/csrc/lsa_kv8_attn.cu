@@ -17,12 +17,14 @@
 // of the step's integer instructions).  Codes become fp16 exactly; Q is divided by its
 // row's power of two and becomes fp16 (exact to 2^-17 of the row's largest
 // element, absolute error 2^-25 of it below that; an e4m3 mma.sync converts
-// both operands to fp16 itself and was slower); P is fp16 with 12 bits of
-// headroom (an entry 2^-26 of the largest still has all its bits).  Scores,
-// softmax sums and outputs are fp32.  The K scale multiplies the scores; the
-// V scale, a power of two, multiplies P relative to the largest V scale seen
-// so far.  The running maximum moves only when a score exceeds it by 2 (in
-// base 2), so most steps skip the rescaling.
+// both operands to fp16 itself and was slower).  P, a probability times its
+// key's V scale, is fp16 in units of its column: the largest such product the
+// column has attended stands between 2^12 and 2^15, so that a product 2^-26 of
+// it still has all its bits, and pages of large values take none from the
+// columns that do not attend them.  Scores, softmax sums and outputs are fp32;
+// the K scale multiplies the scores.  A column's running maximum and unit move
+// only when a score exceeds the maximum by 2 (in base 2) or P would pass 2^15,
+// so most steps skip the rescaling; both move by powers of two, which is exact.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -38,9 +40,10 @@
 namespace lsa {
 
 constexpr int kKv8ListWarps = 8;
-constexpr int kKv8Head = 12;       // log2 of P's headroom: P is at most 2^(12 + 2), fp16 ends at 65504
-constexpr float kKv8Unit = 1.f / (1 << kKv8Head);
-constexpr float kKv8Lazy = 2.f;    // log2 growth that moves the running maximum
+constexpr float kKv8MostE = 4.f;      // a probability above this moves the running maximum
+constexpr float kKv8MostP = 32768.f;  // a P above this the column's unit (fp16 ends at 65504)
+constexpr int kKv8LowP = 12;          // log2 of P, rounded down, of the product that the unit is taken from
+constexpr int kKv8MaxUnit = kKv8LowP - kKv8MinExp;  // largest exponent of 1 / unit: the smallest V scale's, attended whole
 
 struct Kv8AttnArgs {
     const uint16_t* Q;     // [nq, hq, 128], token rows q_stride elements apart
@@ -112,7 +115,7 @@ struct Kv8State {
     float cf[NT][2];        // Q's power of two of columns 2t, 2t + 1
     float o[NT][8][4];
     float m[NT][2], l[NT][2];
-    float vref;             // the V scale that O is relative to
+    float iv[NT][2];        // 1 / unit: P = probability * V scale * iv, O is in units
 };
 
 // Q row of each column (gq within tile nt; NULL: none), dims 32 t .. + 31 on
@@ -155,8 +158,8 @@ __device__ __forceinline__ void kv8_load_q(Kv8State<NT>& s, const uint16_t* cons
             for (int i = 0; i < 4; ++i) s.o[nt][mt][i] = 0.f;
         s.m[nt][0] = s.m[nt][1] = -FLT_MAX;
         s.l[nt][0] = s.l[nt][1] = 0.f;
+        s.iv[nt][0] = s.iv[nt][1] = __uint_as_float((127u + kKv8MaxUnit) << 23);
     }
-    s.vref = 0x1p-100f;
 }
 
 // The lane's 32 codes (dims 32 t .. + 31) of key rows g and g + 8.
@@ -211,55 +214,91 @@ __device__ __forceinline__ void kv8_pv(Kv8State<NT>& s, const Kv8V& v, const uin
 // Key of a step that row g of S^T stands for; row g + 8 is the key two after.
 __device__ __forceinline__ int kv8_key(int gq) { return 4 * (gq >> 1) + (gq & 1); }
 
+// 2^-d, 0 from d = 126 on.
+__device__ __forceinline__ float pow2_down(int d) { return d < 126 ? __uint_as_float((uint32_t)(127 - d) << 23) : 0.f; }
+
 // Softmax of one step.  Scores in base 2, -inf where masked; vs0, vs1: the V
-// scales of rows g and g + 8.  Leaves P^T as B operands in pb.
-template <int NT>
+// scales of rows g and g + 8.  Leaves P^T as B operands in pb.  Scores are taken
+// relative to the maximum before anything else is added: next to it the
+// differences are exact, however far the floats of large scores are apart.
+// ONE_PAGE: all keys of the step have the same V scale.
+template <int NT, bool ONE_PAGE>
 __device__ __forceinline__ void kv8_softmax(Kv8State<NT>& s, const float (&sc)[NT][4], float vs0, float vs1,
                                             uint32_t (&pb)[NT][2]) {
-    bool grew = fmaxf(vs0, vs1) > s.vref;
+    float e[NT][4], p[NT][4];
+    auto probabilities = [&]() {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                e[nt][i] = ex2(sc[nt][i] - s.m[nt][i & 1]);
+                p[nt][i] = e[nt][i] * ((i < 2 ? vs0 : vs1) * s.iv[nt][i & 1]);
+            }
+    };
+    probabilities();
+    float most_e = 0.f, most_p = 0.f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
-        grew = grew || fmaxf(sc[nt][0], sc[nt][2]) - s.m[nt][0] > kKv8Lazy || fmaxf(sc[nt][1], sc[nt][3]) - s.m[nt][1] > kKv8Lazy;
-    if (__any_sync(0xffffffffu, grew)) {
-        // the step's largest V scale: positive floats order as integers
-        const float vmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(vs0, vs1))));
-        const float nref = fmaxf(vmax, s.vref), rv = s.vref / nref;
-        s.vref = nref;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            float mx0 = fmaxf(sc[nt][0], sc[nt][2]), mx1 = fmaxf(sc[nt][1], sc[nt][3]);
+        for (int i = 0; i < 4; ++i) {
+            most_e = fmaxf(most_e, e[nt][i]);
+            most_p = fmaxf(most_p, p[nt][i]);
+        }
+    if (__any_sync(0xffffffffu, most_e > kKv8MostE || most_p > kKv8MostP)) {
+        float top[NT][2], m[NT][2];  // of each column: the largest score, later product; the new maximum
+        auto over_keys = [&]() {
 #pragma unroll
-            for (int off = 4; off < 32; off <<= 1) {
-                mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
-                mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
-            }
-            const float n0 = fmaxf(s.m[nt][0], mx0), n1 = fmaxf(s.m[nt][1], mx1);
-            const float a0 = ex2(s.m[nt][0] - n0), a1 = ex2(s.m[nt][1] - n1);
-            s.m[nt][0] = n0;
-            s.m[nt][1] = n1;
-            s.l[nt][0] *= a0;
-            s.l[nt][1] *= a1;
-            const float f0 = a0 * rv, f1 = a1 * rv;
+            for (int off = 4; off < 32; off <<= 1)
+#pragma unroll
+                for (int i = 0; i < 2 * NT; ++i) top[i >> 1][i & 1] = fmaxf(top[i >> 1][i & 1], __shfl_xor_sync(0xffffffffu, top[i >> 1][i & 1], off));
+        };
+#pragma unroll
+        for (int i = 0; i < 2 * NT; ++i) top[i >> 1][i & 1] = fmaxf(sc[i >> 1][i & 1], sc[i >> 1][2 + (i & 1)]);
+        over_keys();
+#pragma unroll
+        for (int i = 0; i < 2 * NT; ++i) {
+            const int nt = i >> 1, c = i & 1;
+            // a whole number, so that what was summed before is worth 2^-d, d whole
+            m[nt][c] = fmaxf(s.m[nt][c], ceilf(top[nt][c]));
+            top[nt][c] = ONE_PAGE ? ex2(top[nt][c] - m[nt][c]) * vs0
+                                  : fmaxf(ex2(sc[nt][c] - m[nt][c]) * vs0, ex2(sc[nt][2 + c] - m[nt][c]) * vs1);
+        }
+        if (!ONE_PAGE) over_keys();
+#pragma unroll
+        for (int i = 0; i < 2 * NT; ++i) {
+            const int nt = i >> 1, c = i & 1;
+            const int d = (int)fminf(m[nt][c] - s.m[nt][c], 126.f);  // 126 or more: nothing is left
+            // exponents (biased) of iv: what it was, moved with the maximum, and what
+            // brings the step's largest product to 2^12 .. 2^13
+            const int was = (int)(__float_as_uint(s.iv[nt][c]) >> 23);
+            const int keep = d < 126 ? was + d : 255, fit = 254 + kKv8LowP - (int)((__float_as_uint(top[nt][c]) & 0x7FFFFFFFu) >> 23);
+            const int now = min(min(keep, fit), 127 + kKv8MaxUnit);
+            const float f = d < 126 ? pow2_down(was + d - now) : 0.f;
+            s.m[nt][c] = m[nt][c];
+            s.iv[nt][c] = __uint_as_float((uint32_t)now << 23);
+            s.l[nt][c] *= pow2_down(d);
 #pragma unroll
             for (int mt = 0; mt < 8; ++mt) {
-                s.o[nt][mt][0] *= f0; s.o[nt][mt][1] *= f1; s.o[nt][mt][2] *= f0; s.o[nt][mt][3] *= f1;
+                s.o[nt][mt][c] *= f;
+                s.o[nt][mt][2 + c] *= f;
             }
         }
+        probabilities();
     }
-    // 2^12 / vref: a power of two, exactly.  The headroom goes here and not into the
-    // maximum: at scores of 2^25 and more a float's spacing would round m - 12, and
-    // its error be a factor of P.  The differences sc - m are exact next to m.
-    const float iv = __uint_as_float(0x7F000000u + (kKv8Head << 23) - __float_as_uint(s.vref)), w0 = vs0 * iv, w1 = vs1 * iv;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        const float e0 = ex2(sc[nt][0] - s.m[nt][0]), e1 = ex2(sc[nt][1] - s.m[nt][1]);
-        const float e2 = ex2(sc[nt][2] - s.m[nt][0]), e3 = ex2(sc[nt][3] - s.m[nt][1]);
-        s.l[nt][0] += e0 + e2;
-        s.l[nt][1] += e1 + e3;
-        pb[nt][0] = movmatrix_t(pack_f16x2(e0 * w0, e1 * w0));
-        pb[nt][1] = movmatrix_t(pack_f16x2(e2 * w1, e3 * w1));
+        s.l[nt][0] += e[nt][0] + e[nt][2];
+        s.l[nt][1] += e[nt][1] + e[nt][3];
+        pb[nt][0] = movmatrix_t(pack_f16x2(p[nt][0], p[nt][1]));
+        pb[nt][1] = movmatrix_t(pack_f16x2(p[nt][2], p[nt][3]));
     }
 }
+
+// A column's unit: the reciprocal of a power of two, exactly.
+__device__ __forceinline__ float kv8_unit(float iv) { return __uint_as_float(0x7F000000u - __float_as_uint(iv)); }
+
+// f / l, 0 for a state without a key (a NaN stays).
+__device__ __forceinline__ float kv8_over(float f, float l) { return l > 0.f || l != l ? f / l : 0.f; }
 
 // Sum of l over the lanes that share a column.
 template <int NT>
@@ -522,7 +561,7 @@ __device__ __forceinline__ void kv8_step(const Kv8AttnArgs& a, const Kv8Keys<LIS
         }
     }
     uint32_t pb[NT][2];
-    kv8_softmax<NT>(s, x, v0, v1, pb);
+    kv8_softmax<NT, !LIST>(s, x, v0, v1, pb);
     Kv8V v;
     kv8_read_v(slot, v);
     if constexpr (FMT == 0 && !LIST) {
@@ -632,7 +671,7 @@ __global__ void __launch_bounds__(32 * kKv8ListWarps, 2) kv8_list_kernel(Kv8Attn
     uint16_t* os = reinterpret_cast<uint16_t*>(lsm + (threadIdx.x >> 5) * kKv8Warp);
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-        const float l = s.l[0][c], f = l > 0.f || l != l ? s.vref * kKv8Unit / l : 0.f;
+        const float l = s.l[0][c], f = kv8_over(kv8_unit(s.iv[0][c]), l);
 #pragma unroll
         for (int mt = 0; mt < 8; ++mt) {
             os[(2 * tq + c) * kD + 16 * mt + gq] = bf16_bits(s.o[0][mt][c] * f);
@@ -796,9 +835,6 @@ __device__ __forceinline__ int64_t kv8_out_row(const Kv8AttnArgs& a, const Kv8Se
 
 // Partial states are kept as (m, l) and the output that their keys alone would
 // give: it is within V's range, which sums that are yet to be divided leave.
-// f / l, 0 for a state without a key (a NaN stays).
-__device__ __forceinline__ float kv8_over(float f, float l) { return l > 0.f || l != l ? f / l : 0.f; }
-
 __device__ __forceinline__ void kv8_add(float4& acc, const float4& x, float f) {
     acc = make_float4(acc.x + x.x * f, acc.y + x.y * f, acc.z + x.z * f, acc.w + x.w * f);
 }
@@ -960,7 +996,7 @@ __global__ void __launch_bounds__(32 * WARPS, NT == 1 && WARPS == 8 ? 2 : 1) kv8
                 for (int c = 0; c < 2; ++c) {
                     const int col = wid * 8 * NT + 8 * nt + 2 * tq + c;
                     float* p = so(wid) + (8 * nt + 2 * tq + c) * kKv8Pad + gq;
-                    const float f = kv8_over(s.vref * kKv8Unit, s.l[nt][c]);
+                    const float f = kv8_over(kv8_unit(s.iv[nt][c]), s.l[nt][c]);
 #pragma unroll
                     for (int mt = 0; mt < 8; ++mt) {
                         p[16 * mt] = s.o[nt][mt][c] * f;

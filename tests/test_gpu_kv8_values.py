@@ -1,5 +1,5 @@
-"""Attention over the 8-bit cache where the values' magnitudes are large or
-tiny."""
+"""Attention over the 8-bit cache where the values' magnitudes are large, tiny
+or far apart."""
 import numpy as np
 import pytest
 import torch
@@ -51,3 +51,43 @@ def test_values_of_any_magnitude(lsa, fmt, e, form):
     kv, table = one_sequence(lsa, rng.standard_normal((n, 1, 128)), v, 32, fmt)
     q, hq = bf16(rng.standard_normal((nq, G, 128)))
     compare(lsa, form, kv, table, n, q, hq, fmt)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("fmt,apart,first", [("e4m3", 30, True), ("int8", 45, False), ("e4m3", 90, False), ("int8", 70, True)])
+def test_unattended_pages_of_large_values(lsa, fmt, apart, first, form):
+    """Pages whose values are 2^apart larger and that some heads do not attend
+    (their scores are 150 or more below): those heads' outputs keep the precision
+    that the other pages give them."""
+    rng = np.random.default_rng(apart)
+    n, nq, G, page = 512, 16, 4, 32
+    k = rng.standard_normal((n, 1, 128)) * 0.5
+    v = rng.standard_normal((n, 1, 128)) + 0.5
+    large = np.zeros(n, bool)
+    for p in ((0, 1, 7) if first else (5, 14)):
+        large[p * page:(p + 1) * page] = True
+    k[large, :, 0] = 30.0
+    k[~large, :, 0] = 0.0
+    v[large] *= 2.0 ** apart
+    kv, table = one_sequence(lsa, k, v, page, fmt)
+    q = rng.standard_normal((nq, G, 128))
+    q[..., 0] = -60.0                            # 60 * 30 / sqrt(128): 159 below
+    q[:, 2, 0] = 1.0                             # one head attends them
+    q, hq = bf16(q)
+    compare(lsa, form, kv, table, n, q, hq, fmt)
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_scores_that_climb_past_large_values(lsa, form):
+    """The running maximum leaves large pages behind step by step: what was
+    attended first is 2^40 larger and ends with no weight."""
+    rng = np.random.default_rng(77)
+    n, nq, G, page = 640, 16, 4, 16
+    k = rng.standard_normal((n, 1, 128)) * 0.1
+    k[..., 0] = (np.arange(n) // page)[:, None] * 1.0 + 1.0
+    v = (rng.standard_normal((n, 1, 128)) + 0.5) * 2.0 ** (40.0 - np.arange(n) // page)[:, None, None]
+    kv, table = one_sequence(lsa, k, v, page, "e4m3")
+    q = rng.standard_normal((nq, G, 128)) * 0.5
+    q[..., 0] = np.array([30.0, 64.0, 3.0, 100.0])  # a page's scores are up to 8.8 above the one before
+    q, hq = bf16(q)
+    compare(lsa, form, kv, table, n, q, hq, "e4m3")
