@@ -4,7 +4,9 @@ and the appends, forks, truncations and moves that keep it so.
 Host logic only; the codes are written by lsa_kv8_write and moved by
 lsa_kv8_copy_pages.  A page belongs to every sequence whose table names it
 (a reference count); a fork shares the pages of its parent's tokens, and the first
-append of either into a shared page that is still open copies it first.
+append of either into a shared page that is still open copies it first.  Pages
+that `reserve` promised to a writer are never shared: a fork gets its own copy of
+an open page that tokens are still to be written into.
 Free pages are handed out lowest number first, so that `compact` has little
 to move.  The calls are taken from an `ops` object, as in `seqshard`, so that
 the tests run the same logic without a GPU.
@@ -36,10 +38,10 @@ class LibraryOps:
 
 
 class _Sequence:
-    __slots__ = ("pages", "len")
+    __slots__ = ("pages", "len", "reserved")  # reserved: tokens that `advance` may still count
 
     def __init__(self, pages, n):
-        self.pages, self.len = pages, n
+        self.pages, self.len, self.reserved = pages, n, 0
 
 
 class KV8Pages:
@@ -111,10 +113,22 @@ class KV8Pages:
         self._seqs[sid] = _Sequence([], 0)
         return sid
 
-    def fork(self, sid) -> int:
-        """A sequence with the same tokens, sharing their pages."""
+    def fork(self, sid, stream=None) -> int:
+        """A sequence with the same tokens, sharing their pages.  What the parent
+        reserved stays its own: if tokens are still to be written into its open
+        page, the fork gets a copy of that page (LSA_ENOSPACE without a free one)."""
         parent = self._seq(sid)
-        pages = parent.pages[:-(-parent.len // self.kv.page)]  # what it reserved stays its own
+        pages = parent.pages[:-(-parent.len // self.kv.page)]
+        if parent.reserved and parent.len % self.kv.page:
+            if not self._free:
+                raise LSAError(LSA_ENOSPACE, f"fork: sequence {sid} holds reserved tokens and no page is free for its open page's copy")
+            own = heapq.heappop(self._free)
+            try:
+                self.ops.copy(self.kv, [pages[-1]], [own], stream)
+            except BaseException:
+                heapq.heappush(self._free, own)
+                raise
+            pages[-1] = own
         for p in pages:
             self.refs[p] += 1
         new = self.add()
@@ -127,14 +141,14 @@ class KV8Pages:
         del self._seqs[sid]
 
     def truncate(self, sid, n: int):
-        """Keep a sequence's first n tokens (rejected drafts).  An open page
-        keeps its scale."""
+        """Keep a sequence's first n tokens (rejected drafts) and nothing that
+        is reserved.  An open page keeps its scale."""
         seq = self._seq(sid)
         if not 0 <= n <= seq.len:
             raise ValueError(f"truncate: sequence {sid} holds {seq.len} tokens, got {n}")
         keep = -(-n // self.kv.page)
         self._release(seq.pages[keep:])
-        seq.pages, seq.len = seq.pages[:keep], n
+        seq.pages, seq.len, seq.reserved = seq.pages[:keep], n, 0
 
     def _counts(self, what, sids, counts):
         sids = list(sids)
@@ -193,6 +207,12 @@ class KV8Pages:
         for seq, pages in zip(seqs, tables):
             seq.pages = pages
 
+    @staticmethod
+    def _count(seqs, counts):
+        for seq, c in zip(seqs, counts):
+            seq.len += c
+            seq.reserved = max(0, seq.reserved - c)
+
     def append(self, sids, K, V, counts=None, stream=None):
         """Write new tokens: K, V [n, hkv, 128] bf16, counts[i] rows for
         sequence sids[i] (default one each), in order.  LSA_ENOSPACE if the free
@@ -217,8 +237,7 @@ class KV8Pages:
                 self.ops.write(self.kv, K, V, table, start, cu, stream)
 
         self._own("append", seqs, counts, stream, write if shape[0] else None)
-        for seq, c in zip(seqs, counts):
-            seq.len += c
+        self._count(seqs, counts)
 
     def reserve(self, sids, counts=None, stream=None):
         """Pages for the next counts[i] tokens of sequence sids[i] (default one
@@ -226,16 +245,20 @@ class KV8Pages:
         them afterwards.  Tell with `advance` how many were written."""
         seqs, counts = self._counts("reserve", sids, counts)
         self._own("reserve", seqs, counts, stream)
+        for seq, c in zip(seqs, counts):
+            seq.reserved = max(seq.reserved, c)
 
     def advance(self, sids, counts=None):
-        """Count tokens that were written into reserved pages."""
+        """Count tokens that were written into reserved pages.  Refused where
+        one of these pages belongs to another sequence too."""
         sids = list(sids)
         seqs, counts = self._counts("advance", sids, counts)
         for sid, seq, c in zip(sids, seqs, counts):
             if seq.len + c > len(seq.pages) * self.kv.page:
                 raise ValueError(f"advance: sequence {sid} has pages for {len(seq.pages) * self.kv.page} tokens, not {seq.len + c}")
-        for seq, c in zip(seqs, counts):
-            seq.len += c
+            if c > 0 and any(self.refs[p] > 1 for p in seq.pages[seq.len // self.kv.page:-(-(seq.len + c) // self.kv.page)]):
+                raise ValueError(f"advance: sequence {sid} shares a page that the tokens would stand in (reserve them first)")
+        self._count(seqs, counts)
 
     def compact(self, stream=None) -> int:
         """Move the used pages to the lowest numbers.  Returns how many moved;
