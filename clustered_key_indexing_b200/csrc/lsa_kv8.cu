@@ -26,12 +26,18 @@ constexpr int kKv8MinExp = -100;  // exponent of an all-zero page's scale
 // Exponent of the smallest power of two 2^e, e >= kKv8MinExp, with
 // amax <= 2^e * QMAX, from amax's bf16 magnitude bits (8 exponent, 7 mantissa
 // bits): QMAX = 448 = 1.75 * 2^8 (mantissa 96), 127 = 1.984375 * 2^6 (126).
+// int8 ends at 2^121: 127 of it is within half a step of bf16's largest, while
+// 64 times 2^122 would be 2^128.
 template <int FMT>
 __device__ __forceinline__ int kv8_exp(uint32_t m) {
     const int E = (int)(m >> 7) - 127, f = (int)(m & 127u);
-    const int e = FMT == 0 ? E - 8 + (f > 96) : E - 6 + (f > 126);
+    const int e = FMT == 0 ? E - 8 + (f > 96) : min(E - 6 + (f > 126), 121);
     return m == 0u || e < kKv8MinExp ? kKv8MinExp : e;
 }
+
+// Magnitude bits from which on int8's codes need a clamp: bf16's largest, which
+// is 127.5 times 2^121.
+constexpr uint32_t kKv8Ends = 0x7F7Fu;
 
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
@@ -52,7 +58,7 @@ __device__ __forceinline__ uint32_t kv8_pack4(float a, float b, float c, float d
     }
 }
 
-// The same for finite values within the format's range.
+// The same for finite values within the format's range (below kKv8Ends).
 template <int FMT>
 __device__ __forceinline__ uint32_t kv8_pack4_finite(float a, float b, float c, float d) {
     if constexpr (FMT == 0) {
@@ -62,6 +68,13 @@ __device__ __forceinline__ uint32_t kv8_pack4_finite(float a, float b, float c, 
         auto q = [](float x) -> uint32_t { return __float_as_uint(x + 12582912.f); };
         return __byte_perm(__byte_perm(q(a), q(b), 0x0040), __byte_perm(q(c), q(d), 0x0040), 0x5410);
     }
+}
+
+// Four e4m3 codes at the scale 2^120, where 256 and more would not be finite in
+// fp32: magnitudes of 240 (0x77) at most, NaN (0x7F) stays.
+__device__ __forceinline__ uint32_t kv8_cap4(uint32_t w) {
+    const uint32_t m = w & 0x7F7F7F7Fu, over = __vcmpgtu4(m, 0x77777777u) & ~__vcmpeq4(m, 0x7F7F7F7Fu);
+    return (w & ~over) | (((w & 0x80808080u) | 0x77777777u) & over);
 }
 
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
@@ -251,8 +264,8 @@ __global__ void __launch_bounds__(256, PASSES <= 8 ? 5 : 2) kv8_write_kernel(Kv8
         uint32_t mx = 0u;
 #pragma unroll
         for (int i = 0; i < 8; ++i) mx = max(mx, s_max[j][i]);
-        const bool finite = mx < 0x7F80u;
-        if (!finite) {  // the largest finite magnitude
+        const bool finite = mx < kKv8Ends;
+        if (!finite) {  // infinities, NaN or nearly: the largest finite magnitude
             mx = 0u;
 #pragma unroll
             for (int i = 0; i < PASSES; ++i) {
@@ -295,9 +308,10 @@ __global__ void __launch_bounds__(256, PASSES <= 8 ? 5 : 2) kv8_write_kernel(Kv8
                 y[2 * e2] = __uint_as_float(w[e2] << 16) * inv;
                 y[2 * e2 + 1] = __uint_as_float(w[e2] & 0xFFFF0000u) * inv;
             }
-            *reinterpret_cast<uint2*>(dst + r * kD + c * 8) =
-                finite ? make_uint2(kv8_pack4_finite<FMT>(y[0], y[1], y[2], y[3]), kv8_pack4_finite<FMT>(y[4], y[5], y[6], y[7]))
-                       : make_uint2(kv8_pack4<FMT>(y[0], y[1], y[2], y[3]), kv8_pack4<FMT>(y[4], y[5], y[6], y[7]));
+            uint2 w8 = finite ? make_uint2(kv8_pack4_finite<FMT>(y[0], y[1], y[2], y[3]), kv8_pack4_finite<FMT>(y[4], y[5], y[6], y[7]))
+                              : make_uint2(kv8_pack4<FMT>(y[0], y[1], y[2], y[3]), kv8_pack4<FMT>(y[4], y[5], y[6], y[7]));
+            if (FMT == 0 && s >= 0x1p120f) w8 = make_uint2(kv8_cap4(w8.x), kv8_cap4(w8.y));
+            *reinterpret_cast<uint2*>(dst + r * kD + c * 8) = w8;
         }
         if (tid == 0) sp[head(j) * 2 + is_v(j)] = s;
     }

@@ -302,7 +302,7 @@ lsa_status lsa_select_attn(const uint16_t* Q, const uint16_t* K,
  *   K, V   [n_pages, hkv, page, d_head] codes: OCP e4m3 (fmt LSA_KV8_E4M3) or
  *          two's complement int8 in -127 .. 127 (LSA_KV8_INT8);
  *   scale  [n_pages, hkv, 2] fp32, K's and V's: powers of two 2^e with
- *          -100 <= e <= 120.  A code's value is code * scale.
+ *          -100 <= e <= 120 (int8: 121).  A code's value is code * scale.
  * Token t of sequence b is row t % page of page table[b, t / page]; `table`
  * is int32 [n_seq, max_pages] on the device, entries behind a sequence's last
  * page are not read.  Sequences may share pages (a forked prefix): reading
@@ -644,12 +644,13 @@ lsa_status lsa_lse_combine(const float* O_parts, const float* lse_parts, int32_t
  * on the device.
  * Per page, kv-head and tensor, with QMAX = 448 (e4m3) or 127 (int8):
  *   a page whose first row is written: scale = the smallest 2^e, e >= -100,
- *     with max |x| <= 2^e QMAX over the finite new values;
+ *     with max |x| <= 2^e QMAX over the finite new values (int8: e <= 121);
  *   a page that was open: scale = max(its scale, that power of two); if it
  *     grew, the rows written before are rounded again at the new scale (an
  *     e4m3 code keeps its value unless it turns subnormal);
- *   code = x / scale rounded to nearest even, saturated (infinities too); NaN
- *     gives the e4m3 NaN code, and 0 in int8.
+ *   code = x / scale rounded to nearest even, saturated at QMAX (infinities
+ *     too; e4m3 at the scale 2^120 at 240), so that every code's value is finite
+ *     in fp32; NaN gives the e4m3 NaN code, and 0 in int8.
  * Rows behind the new tokens keep their bytes.  No two new tokens may share a
  * page unless they belong to the same sequence.
  */
