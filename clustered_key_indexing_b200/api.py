@@ -697,10 +697,17 @@ def _rows(t, name, heads, dev: int):
     return t.data_ptr(), ld, n, h
 
 
+def _of_device(stream, dev: int):
+    if stream.device_index != dev:
+        raise ValueError(f"stream: expected one of device {dev}, got one of device {stream.device_index}")
+
+
 def _launch(kv, stream, call, *args):
     """call(*args, stream handle) with the cache's device current; its status."""
     dev = kv.index
     _on_gpu(dev)
+    if stream is not None:
+        _of_device(stream, dev)
     if torch._C._cuda_getDevice() != dev:
         with torch.cuda.device(dev):
             return _launch(kv, stream, call, *args)
@@ -747,8 +754,7 @@ def _kv8_attend(kv, name, call, args, need, Q, n, h, O, lse, ws, stream):
     gave or that are made here, the launch, the status."""
     dev = kv.index
     if stream is not None:
-        if stream.device_index != dev:
-            raise ValueError(f"stream: expected one of device {dev}, got one of device {stream.device_index}")
+        _of_device(stream, dev)
         # what is made here is `stream`'s memory: a block that the current stream
         # gave back may still be in use there
         here = torch.cuda.current_stream(dev)
