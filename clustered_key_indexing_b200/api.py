@@ -795,7 +795,9 @@ def kv8_attn(Q: torch.Tensor, kv: KV8, table: torch.Tensor, lens: torch.Tensor, 
     `sinks`).  Q [nq, hq, 128] bf16, sequence b's rows cu[b] .. cu[b + 1] - 1
     (cu None: one each); lens counts the new tokens too.  ws: optional, uint8,
     used if it is large enough.  Returns (O bf16 [nq, hq, 128], lse fp32
-    [nq, hq], base 2)."""
+    [nq, hq], base 2).  Rows of Q that no sequence claims (before cu[0], from
+    cu[-1] on) are not computed: an O and lse given here keep what they hold
+    there, those made here hold nothing of meaning."""
     dev, L = kv.index, lib()
     pq, ld, nq, hq = _rows(Q, "Q", None, dev)
     shape = table.shape
