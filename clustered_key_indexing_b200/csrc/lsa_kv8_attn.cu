@@ -24,7 +24,7 @@
 // columns that do not attend them.  Scores, softmax sums and outputs are fp32;
 // the K scale multiplies the scores.  A column's running maximum and unit move
 // only when a score exceeds the maximum by 2 (in base 2) or P would pass 2^15,
-// so most steps skip the rescaling; both move by powers of two, which is exact.
+// so most steps skip the rescaling.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -42,8 +42,9 @@ namespace lsa {
 constexpr int kKv8ListWarps = 8;
 constexpr float kKv8MostE = 4.f;      // a probability above this moves the running maximum
 constexpr float kKv8MostP = 32768.f;  // a P above this the column's unit (fp16 ends at 65504)
-constexpr int kKv8LowP = 12;          // log2 of P, rounded down, of the product that the unit is taken from
-constexpr int kKv8MaxUnit = kKv8LowP - kKv8MinExp;  // largest exponent of 1 / unit: the smallest V scale's, attended whole
+constexpr float kKv8TopP = 4096.f;    // P of the product that the unit is taken from
+constexpr float kKv8MaxIv = 0x1p112f; // largest 1 / unit: of the smallest V scale, 2^-100, attended whole
+static_assert(kKv8MinExp == -100, "the smallest V scale");
 
 struct Kv8AttnArgs {
     const uint16_t* Q;     // [nq, hq, 128], token rows q_stride elements apart
@@ -158,7 +159,7 @@ __device__ __forceinline__ void kv8_load_q(Kv8State<NT>& s, const uint16_t* cons
             for (int i = 0; i < 4; ++i) s.o[nt][mt][i] = 0.f;
         s.m[nt][0] = s.m[nt][1] = -FLT_MAX;
         s.l[nt][0] = s.l[nt][1] = 0.f;
-        s.iv[nt][0] = s.iv[nt][1] = __uint_as_float((127u + kKv8MaxUnit) << 23);
+        s.iv[nt][0] = s.iv[nt][1] = kKv8MaxIv;
     }
 }
 
@@ -268,14 +269,14 @@ __device__ __forceinline__ void kv8_softmax(Kv8State<NT>& s, const float (&sc)[N
         for (int i = 0; i < 2 * NT; ++i) {
             const int nt = i >> 1, c = i & 1;
             const int d = (int)fminf(m[nt][c] - s.m[nt][c], 126.f);  // 126 or more: nothing is left
-            // exponents (biased) of iv: what it was, moved with the maximum, and what
-            // brings the step's largest product to 2^12 .. 2^13
-            const int was = (int)(__float_as_uint(s.iv[nt][c]) >> 23);
-            const int keep = d < 126 ? was + d : 255, fit = 254 + kKv8LowP - (int)((__float_as_uint(top[nt][c]) & 0x7FFFFFFFu) >> 23);
-            const int now = min(min(keep, fit), 127 + kKv8MaxUnit);
-            const float f = d < 126 ? pow2_down(was + d - now) : 0.f;
+            // 1 / unit: what it was, moved with the maximum, or what makes the step's
+            // largest product 2^12, without rounding: where one key outweighs the
+            // others, its P is exact
+            const float was = s.iv[nt][c], keep = d < 126 ? was * __uint_as_float((uint32_t)(127 + d) << 23) : CUDART_INF_F;
+            const float now = fminf(fminf(keep, __fdividef(kKv8TopP, top[nt][c])), kKv8MaxIv);
+            const float f = now == keep ? 1.f : __fdividef(now, was) * pow2_down(d);
             s.m[nt][c] = m[nt][c];
-            s.iv[nt][c] = __uint_as_float((uint32_t)now << 23);
+            s.iv[nt][c] = now;
             s.l[nt][c] *= pow2_down(d);
 #pragma unroll
             for (int mt = 0; mt < 8; ++mt) {
@@ -293,9 +294,6 @@ __device__ __forceinline__ void kv8_softmax(Kv8State<NT>& s, const float (&sc)[N
         pb[nt][1] = movmatrix_t(pack_f16x2(p[nt][2], p[nt][3]));
     }
 }
-
-// A column's unit: the reciprocal of a power of two, exactly.
-__device__ __forceinline__ float kv8_unit(float iv) { return __uint_as_float(0x7F000000u - __float_as_uint(iv)); }
 
 // f / l, 0 for a state without a key (a NaN stays).
 __device__ __forceinline__ float kv8_over(float f, float l) { return l > 0.f || l != l ? f / l : 0.f; }
@@ -671,7 +669,7 @@ __global__ void __launch_bounds__(32 * kKv8ListWarps, 2) kv8_list_kernel(Kv8Attn
     uint16_t* os = reinterpret_cast<uint16_t*>(lsm + (threadIdx.x >> 5) * kKv8Warp);
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-        const float l = s.l[0][c], f = kv8_over(kv8_unit(s.iv[0][c]), l);
+        const float l = s.l[0][c], f = kv8_over(1.f / s.iv[0][c], l);
 #pragma unroll
         for (int mt = 0; mt < 8; ++mt) {
             os[(2 * tq + c) * kD + 16 * mt + gq] = bf16_bits(s.o[0][mt][c] * f);
@@ -996,7 +994,7 @@ __global__ void __launch_bounds__(32 * WARPS, NT == 1 && WARPS == 8 ? 2 : 1) kv8
                 for (int c = 0; c < 2; ++c) {
                     const int col = wid * 8 * NT + 8 * nt + 2 * tq + c;
                     float* p = so(wid) + (8 * nt + 2 * tq + c) * kKv8Pad + gq;
-                    const float f = kv8_over(kv8_unit(s.iv[nt][c]), s.l[nt][c]);
+                    const float f = kv8_over(1.f / s.iv[nt][c], s.l[nt][c]);
 #pragma unroll
                     for (int mt = 0; mt < 8; ++mt) {
                         p[16 * mt] = s.o[nt][mt][c] * f;
