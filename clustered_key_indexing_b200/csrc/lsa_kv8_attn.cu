@@ -831,19 +831,58 @@ __device__ __forceinline__ int64_t kv8_out_row(const Kv8AttnArgs& a, const Kv8Se
     return (q.q0 + (cc >> a.lgG)) * (a.G * a.hkv) + g * a.G + (cc & (a.G - 1));
 }
 
+constexpr int kKv8Cluster = 8;  // CTAs of a cluster at most
+
 // Partial states are kept as (m, l) and the output that their keys alone would
-// give: it is within V's range, which sums that are yet to be divided leave.
-__device__ __forceinline__ void kv8_add(float4& acc, const float4& x, float f) {
-    acc = make_float4(acc.x + x.x * f, acc.y + x.y * f, acc.z + x.z * f, acc.w + x.w * f);
-}
+// give, which is within V's range.  Sums of l times that are not, before they are
+// divided by l: joins scale them by 2^-k, with 2^k at least the row's l (a key's
+// probability is 4 at most).
+struct Kv8Join {
+    float down, up;  // 2^-k, 2^k
+    float M, l;
+    float4 acc;
+
+    __device__ __forceinline__ explicit Kv8Join(int chunks) {
+        const int k = 39 - __clz(chunks);  // 2^k > 4 * 32 * chunks
+        down = __uint_as_float((uint32_t)(127 - k) << 23);
+        up = __uint_as_float((uint32_t)(127 + k) << 23);
+        M = -FLT_MAX;
+        l = 0.f;
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    // One state more: x times weight, both relative to M.
+    __device__ __forceinline__ void add(const float4& x, float weight) {
+        l += weight;
+        weight *= down;
+        acc = make_float4(acc.x + x.x * weight, acc.y + x.y * weight, acc.z + x.z * weight, acc.w + x.w * weight);
+    }
+    // A state with a maximum of its own.
+    __device__ __forceinline__ void add(const float4& x, float2 ml) {
+        const float m = fmaxf(M, ml.x), f = ex2(M - m);
+        acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+        l *= f;
+        M = m;
+        add(x, ml.y * ex2(ml.x - m));
+    }
+    // Another join of the same row.
+    __device__ __forceinline__ void merge(const float4& x, float2 ml) {
+        const float m = fmaxf(M, ml.x), f = ex2(M - m), g = ex2(ml.x - m);
+        acc = make_float4(acc.x * f + x.x * g, acc.y * f + x.y * g, acc.z * f + x.z * g, acc.w * f + x.w * g);
+        l = l * f + ml.y * g;
+        M = m;
+    }
+    __device__ __forceinline__ float4 out() const {
+        const float f = kv8_over(up, l);
+        return make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+    }
+};
 
 // Four elements of one output row (dims d .. d + 3).
-__device__ __forceinline__ void kv8_store(const Kv8AttnArgs& a, int64_t orow, int d, float4 x, float m, float l) {
+__device__ __forceinline__ void kv8_store(const Kv8AttnArgs& a, int64_t orow, int d, const Kv8Join& j) {
+    const float4 x = j.out();
     *reinterpret_cast<uint2*>(a.O + orow * kD + d) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
-    if (d == 0 && a.lse) a.lse[orow] = l > 0.f || l != l ? m + log2f(l) : -CUDART_INF_F;
+    if (d == 0 && a.lse) a.lse[orow] = j.l > 0.f || j.l != j.l ? j.M + log2f(j.l) : -CUDART_INF_F;
 }
-
-constexpr int kKv8Cluster = 8;  // CTAs of a cluster at most
 
 // Number of this CTA in its cluster, CTAs of the cluster, the cluster's barrier
 // (which orders shared memory), and a load from CTA `rank`'s shared memory.
@@ -889,6 +928,10 @@ __global__ void __launch_bounds__(32 * WARPS, NT == 1 && WARPS == 8 ? 2 : 1) kv8
     constexpr bool CLUSTER = WARPS != kKv8Warps || NT == 2;  // may run as clusters
     __shared__ __align__(8) float sml[WARPS * 8 * NT * 2];                     // (m, l) of every warp's columns
     __shared__ __align__(8) float cml[CLUSTER ? 8 * NT * 2 : 2];               // and of the CTA's, for its cluster
+    // what a CTA of the stream knows of its row stands here while the keys are
+    // walked, for which every register is needed (a CTA that has one row only
+    // would wait for it: 777 tokens 6.8 us, 6.4 without)
+    __shared__ struct { Kv8Seq q; int64_t b, w, w1; int32_t g, cg, pad; bool whole, begins; } s_row;
     const uint32_t ring = smem_u32(ksm) + (threadIdx.x >> 5) * kKv8Warp;
     // a warp's sums go where its ring was: [8 NT][kKv8Pad] floats
     auto so = [&](int w) { return reinterpret_cast<float*>(ksm + w * kKv8Warp); };
@@ -896,7 +939,8 @@ __global__ void __launch_bounds__(32 * WARPS, NT == 1 && WARPS == 8 ? 2 : 1) kv8
     // a CTA's sums of column c, for its cluster: behind the sums in warp c % 8's ring
     auto sc = [&](int c) { return ksm + (c & 7) * kKv8Warp + 8 * NT * kKv8Pad * 4 + (c >> 3) * kD * 4; };
     static_assert(8 * NT * kKv8Pad * 4 + NT * kD * 4 <= kKv8Warp, "sums fit");
-    const bool own = WARPS != kKv8Warps || a.own;  // a CTA or a cluster for each row
+    constexpr bool kStream = WARPS == kKv8Warps;   // may take pieces of the stream
+    const bool own = !kStream || a.own;            // a CTA or a cluster for each row
     const int csize = CLUSTER && own ? (int)cluster_size() : 1;
     Kv8Seq q;
     int64_t b, w0 = 0, w1 = 0;
@@ -947,8 +991,9 @@ __global__ void __launch_bounds__(32 * WARPS, NT == 1 && WARPS == 8 ? 2 : 1) kv8
             n = max(0, u0 + nu - pad) - t0;
             w += nu;
         }
-        const int g = r / q.groups, cg = r % q.groups;
+        int g = r / q.groups, cg = r % q.groups;
         const int ta = t0 + wid, tb = t0 + n;  // neighbouring chunks at the same time: whole pages of DRAM
+        if (kStream && tid == 0) s_row = {q, b, w, w1, g, cg, pad, whole, begins};
 
         if (ta < tb) {
             Kv8State<NT> s;
@@ -1009,33 +1054,36 @@ __global__ void __launch_bounds__(32 * WARPS, NT == 1 && WARPS == 8 ? 2 : 1) kv8
             }
         }
         __syncthreads();
+        if (kStream) {
+            q = s_row.q; b = s_row.b; w = s_row.w; w1 = s_row.w1;
+            g = s_row.g; cg = s_row.cg; pad = s_row.pad; whole = s_row.whole; begins = s_row.begins;
+        }
         float* part = a.part + ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * kv8_part_floats<NT>();
         for (int e = tid; e < 8 * NT * kD / 4; e += 32 * WARPS) {  // four sums of a column
             const int c = e / (kD / 4), dim = e % (kD / 4) * 4;
             const int64_t orow = kv8_out_row<NT>(a, q, cg, g, c);
             if (orow < 0) continue;
-            float M = -FLT_MAX, l = 0.f, weight[WARPS];
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            Kv8Join join(q.chunks);
+            float weight[WARPS];
 #pragma unroll
-            for (int i = 0; i < WARPS; ++i) M = fmaxf(M, sml[2 * (i * 8 * NT + c)]);
+            for (int i = 0; i < WARPS; ++i) join.M = fmaxf(join.M, sml[2 * (i * 8 * NT + c)]);
 #pragma unroll
             for (int i = 0; i < WARPS; ++i) {
                 const float2 ml = *reinterpret_cast<const float2*>(sml + 2 * (i * 8 * NT + c));
-                weight[i] = ml.y == -1.f ? 0.f : ml.y * ex2(ml.x - M);
-                l += weight[i];
+                weight[i] = ml.y == -1.f ? 0.f : ml.y * ex2(ml.x - join.M);
             }
-            const float f = kv8_over(1.f, l);
 #pragma unroll
-            for (int i = 0; i < WARPS; ++i)  // a warp without a chunk has written no sums
-                if (weight[i] != 0.f) kv8_add(acc, *reinterpret_cast<const float4*>(so(i) + c * kKv8Pad + dim), weight[i] * f);
+            for (int i = 0; i < WARPS; ++i) {
+                if (weight[i] != 0.f) join.add(*reinterpret_cast<const float4*>(so(i) + c * kKv8Pad + dim), weight[i]);
+            }
             if (CLUSTER && csize > 1) {
-                *reinterpret_cast<float4*>(sc(c) + dim * 4) = acc;
-                if (dim == 0) *reinterpret_cast<float2*>(cml + 2 * c) = make_float2(M, l);
+                *reinterpret_cast<float4*>(sc(c) + dim * 4) = join.out();
+                if (dim == 0) *reinterpret_cast<float2*>(cml + 2 * c) = make_float2(join.M, join.l);
             } else if (whole) {
-                kv8_store(a, orow, dim, acc, M, l);
+                kv8_store(a, orow, dim, join);
             } else {
-                *reinterpret_cast<float4*>(part + c * kD + dim) = acc;
-                if (dim == 0) *reinterpret_cast<float2*>(part + 8 * NT * kD + 2 * c) = make_float2(M, l);
+                *reinterpret_cast<float4*>(part + c * kD + dim) = join.out();
+                if (dim == 0) *reinterpret_cast<float2*>(part + 8 * NT * kD + 2 * c) = make_float2(join.M, join.l);
             }
         }
         if (CLUSTER && csize > 1) {
@@ -1045,29 +1093,22 @@ __global__ void __launch_bounds__(32 * WARPS, NT == 1 && WARPS == 8 ? 2 : 1) kv8
                 const int64_t orow = kv8_out_row<NT>(a, q, cg, g, c);
                 if (orow < 0) continue;
                 const uint32_t pm = smem_u32(cml + 2 * c), ps = smem_u32(sc(c) + dim * 4);
+                Kv8Join join(q.chunks);
                 float2 ml[kKv8Cluster];
                 float4 x[kKv8Cluster];
-                float M = -FLT_MAX, l = 0.f;
-                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int i = 0; i < kKv8Cluster; ++i) {
                     ml[i] = make_float2(-FLT_MAX, 0.f);
-                    x[i] = acc;
+                    x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
                     if (i < csize) {
                         ml[i] = peer_f2(peer_smem(pm, i));
                         x[i] = peer_f4(peer_smem(ps, i));
                     }
-                    M = fmaxf(M, ml[i].x);
+                    join.M = fmaxf(join.M, ml[i].x);
                 }
 #pragma unroll
-                for (int i = 0; i < kKv8Cluster; ++i) {
-                    ml[i].y *= ex2(ml[i].x - M);
-                    l += ml[i].y;
-                }
-                const float f = kv8_over(1.f, l);
-#pragma unroll
-                for (int i = 0; i < kKv8Cluster; ++i) kv8_add(acc, x[i], ml[i].y * f);
-                kv8_store(a, orow, dim, acc, M, l);
+                for (int i = 0; i < kKv8Cluster; ++i) join.add(x[i], ml[i].y * ex2(ml[i].x - join.M));
+                kv8_store(a, orow, dim, join);
             }
             cluster_barrier();  // nobody leaves while others read its sums
             return;
@@ -1077,34 +1118,19 @@ __global__ void __launch_bounds__(32 * WARPS, NT == 1 && WARPS == 8 ? 2 : 1) kv8
     }
 }
 
-// One column of n partial states, of which the first is CTA c's slot 1 and the
-// others the slots 0 of the CTAs after it: (M, l) of all of them, and a lane's
-// four elements of the states i0, i0 + di, ... weighted by their share of l.
+// One column of n partial states, a lane four of its elements: states i0, i0 +
+// di, ... of which the first is CTA c's slot 1 and the others the slots 0 of the
+// CTAs after it.
 template <int NT>
-__device__ __forceinline__ float4 kv8_join_column(const Kv8AttnArgs& a, int64_t c, int col, int i0, int di, int n, float& M,
-                                                  float& l) {
+__device__ __forceinline__ void kv8_join_column(const Kv8AttnArgs& a, int64_t c, int col, int i0, int di, int n, Kv8Join& join) {
+    constexpr int kPart = kv8_part_floats<NT>();
     const int lane = threadIdx.x & 31;
-    auto state = [&](int i) { return a.part + (2 * (c + i) + (i == 0)) * kv8_part_floats<NT>(); };
-    auto ml_of = [&](int i) { return *reinterpret_cast<const float2*>(state(i) + 8 * NT * kD + 2 * col); };
-    M = -FLT_MAX;
-    l = 0.f;
-    for (int i = lane; i < n; i += 32) M = fmaxf(M, ml_of(i).x);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    for (int i = lane; i < n; i += 32) {
-        const float2 ml = ml_of(i);
-        l += ml.y * ex2(ml.x - M);
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-    const float f = kv8_over(1.f, l);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int i = i0; i < n; i += di) {
-        const float2 ml = ml_of(i);
-        kv8_add(acc, *reinterpret_cast<const float4*>(state(i) + col * kD + 4 * lane), ml.y * ex2(ml.x - M) * f);
+        const float* p = a.part + (2 * (c + i) + (i == 0)) * kPart;
+        const float2 ml = *reinterpret_cast<const float2*>(p + 8 * NT * kD + 2 * col);
+        join.add(*reinterpret_cast<const float4*>(p + col * kD + 4 * lane), ml);
     }
-    return acc;
 }
 
 // Joins the row that crosses the end of CTA c's range, if that row began
@@ -1130,23 +1156,25 @@ __global__ void __launch_bounds__(32 * kKv8Warps) kv8_join_kernel(Kv8AttnArgs a,
         for (int col = wid; col < 8 * NT; col += kKv8Warps) {
             const int64_t orow = kv8_out_row<NT>(a, q, cg, g, col);
             if (orow < 0) return;
-            float M, l;
-            const float4 x = kv8_join_column<NT>(a, c, col, 0, 1, n, M, l);
-            kv8_store(a, orow, 4 * lane, x, M, l);
+            Kv8Join join(q.chunks);
+            kv8_join_column<NT>(a, c, col, 0, 1, n, join);
+            kv8_store(a, orow, 4 * lane, join);
         }
         return;
     }
     const int64_t orow = kv8_out_row<NT>(a, q, cg, g, blockIdx.y);
     if (orow < 0) return;
     __shared__ float4 s_acc[kKv8Warps][32];
-    float M, l;
-    s_acc[wid][lane] = kv8_join_column<NT>(a, c, blockIdx.y, wid, kKv8Warps, n, M, l);
+    __shared__ float2 s_ml[kKv8Warps];
+    Kv8Join join(q.chunks);
+    kv8_join_column<NT>(a, c, blockIdx.y, wid, kKv8Warps, n, join);
+    s_acc[wid][lane] = join.acc;
+    if (lane == 0) s_ml[wid] = make_float2(join.M, join.l);
     __syncthreads();
     if (wid > 0) return;
-    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < kKv8Warps; ++i) kv8_add(sum, s_acc[i][lane], 1.f);
-    kv8_store(a, orow, 4 * lane, sum, M, l);
+    for (int i = 1; i < kKv8Warps; ++i) join.merge(s_acc[i][lane], s_ml[i]);
+    kv8_store(a, orow, 4 * lane, join);
 }
 
 // ------------------------------------------------------------- host side
