@@ -16,8 +16,8 @@
 // leaves V's keys (byte permutes of row-wise loads in its place cost an eighth
 // of the step's integer instructions).  Codes become fp16 exactly; Q is divided by its
 // row's power of two and becomes fp16 (exact to 2^-17 of the row's largest
-// element, absolute error 2^-25 of it below that; an e4m3 mma.sync converts
-// both operands to fp16 itself and was slower).  P, a probability times its
+// element, absolute error 2^-25 of it below that; with an e4m3 mma.sync for S
+// 1000 index rows took 1127 us in place of 960).  P, a probability times its
 // key's V scale, is fp16 in units of its column: the largest such product the
 // column has attended stands between 2^12 and 2^15, so that a product 2^-26 of
 // it still has all its bits, and pages of large values take none from the
@@ -641,12 +641,14 @@ struct Kv8Walk {
 // Many rows: one warp per (query, kv-head), kv-head major so that the warps
 // resident at one time read one head's rows, which keeps them in L2.  A step
 // is about 240 instructions, 115 of them integer and conversion (64 turn codes
-// into fp16, two cycles each): 60% of that pipe's cycles, 62% of the issue slots
-// and 61% of the L1 data pipe are used, the tensor pipe a third; the copies alone
-// take 324 us of the 570.  1000 rows x 8 kv-heads of 3076 entries: 570 us, 11.2
+// into fp16, two cycles each): 59% of that pipe's cycles, 62% of the issue slots
+// and 62% of the L1 data pipe are used, the tensor pipe a third; the copies alone
+// take 324 us.  1000 rows x 8 kv-heads of 3076 entries: 561 us captured, 11.4
 // TB/s from L2 (bf16 rows of the same keys are twice the bytes; int8 codes, five
-// instructions for four values instead of two, 708).  Two steps interleaved with
-// 12 warps an SM took 686 us instead of 603, 20 warps of 96 registers 684.
+// instructions for four values instead of two, 729).  A third of the entries are
+// windows that neighbouring queries share; each reads its own.  Two steps
+// interleaved with 12 warps an SM took 686 us instead of 603, 20 warps of 96
+// registers 684.
 template <int FMT>
 __global__ void __launch_bounds__(32 * kKv8ListWarps, 2) kv8_list_kernel(Kv8AttnArgs a) {
     const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
@@ -696,11 +698,13 @@ __global__ void __launch_bounds__(32 * kKv8ListWarps, 2) kv8_list_kernel(Kv8Attn
 // CTA of its own instead (own > 0), or where rows are few a cluster of 2, 4 or 8,
 // whose CTAs take equal shares and join their sums through one another's shared
 // memory: no second kernel, no workspace.  8 rows of 282 chunks (9000 tokens):
-// 11.6 us, 16.7 in the stream (captured; called one by one 14.4 and 24.2).
+// 12.1 us, 17.8 in the stream (captured).  A row's bound comes from the table's
+// width: 777 tokens take 6.8 us in a table of their size, 11.1 in one for 128K.
 //
-// Bound by HBM: a million tokens of 8 kv-heads (2.15 GB) in 333 to 345 us, 32
-// sequences of 2K to 32K tokens (1.21 GB) in 191 us, 6.3 TB/s; the warps of a
-// CTA take neighbouring chunks, so that it reads whole pages at a time.
+// Bound by HBM (captured, calls on the same cache): a million tokens of 8
+// kv-heads (2.15 GB) in 340 to 350 us, 32 sequences of 2K to 32K tokens (1.21 GB)
+// in 193 us, 6.2 TB/s; the warps of a CTA take neighbouring chunks, so that it
+// reads whole pages at a time.
 struct Kv8Seq {
     int64_t base;     // first chunk of the sequence in the stream
     int32_t chunks;   // chunks of each of its rows
@@ -743,8 +747,8 @@ __device__ __forceinline__ void kv8_seq(const Kv8AttnArgs& a, int64_t b, Kv8Seq&
 // What a row costs a CTA of the stream beside its chunks, in chunks: its last
 // warp is waited for, its sums are joined, the next one's copies begin.  It
 // counts in the shares where they are long enough (kKv8Padded chunks a CTA), or
-// CTAs with many short rows would come last (64 sequences of 480 to 8000 tokens
-// 98 us, 124 without; 8 and 32 in place of 16 104 and 99).
+// CTAs with many short rows would come last (64 sequences of 480 to 8000 tokens,
+// one call after another: 98 us, 124 without; 8 and 32 in place of 16 104 and 99).
 constexpr int kKv8RowCost = 16, kKv8Padded = 64;
 
 // A sequence's share of a stream: its chunks and its rows' cost, or (ROWS) its rows.
@@ -1185,7 +1189,12 @@ constexpr int kKv8Least = 8;
 template <int NT>
 static int kv8_ctas() { return num_sms() * (NT == 1 ? 2 : 1); }
 
-// Columns per warp step: 16 when a sequence has on average more than 8.
+// Columns per warp step: 16 when a sequence has on average more than 8, which
+// halves what is read; where little is, 8 columns and twice the rows are quicker
+// by up to 1.7 us (us, 16 / 8 columns, captured; 8 kv-heads of 4 heads unless said
+// otherwise: 4 new tokens on 128K 76 / 106, 32 x 5 on 32K 755 / 969, 4 x 64 on 4K
+// 133 / 159; 2 kv-heads of 8 heads, a window of 1024: 16 x 5 16.6 / 17.2, 64 x 5
+// 45 / 41, 1 x 5 10.0 / 8.5).
 static int kv8_nt(int64_t nq, int64_t n_seq, int G) { return nq * G > 8 * n_seq ? 2 : 1; }
 
 // A kernel's dynamic shared memory limit, raised once a device.
