@@ -233,7 +233,8 @@ __device__ __forceinline__ void kv8_softmax(Kv8State<NT>& s, const float (&sc)[N
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 e[nt][i] = ex2(sc[nt][i] - s.m[nt][i & 1]);
-                p[nt][i] = e[nt][i] * ((i < 2 ? vs0 : vs1) * s.iv[nt][i & 1]);
+                // in this order: where e is 0 so is P, although V scale / unit may overflow
+                p[nt][i] = e[nt][i] * (i < 2 ? vs0 : vs1) * s.iv[nt][i & 1];
             }
     };
     probabilities();
@@ -274,7 +275,7 @@ __device__ __forceinline__ void kv8_softmax(Kv8State<NT>& s, const float (&sc)[N
             // others, its P is exact
             const float was = s.iv[nt][c], keep = d < 126 ? was * __uint_as_float((uint32_t)(127 + d) << 23) : CUDART_INF_F;
             const float now = fminf(fminf(keep, __fdividef(kKv8TopP, top[nt][c])), kKv8MaxIv);
-            const float f = now == keep ? 1.f : __fdividef(now, was) * pow2_down(d);
+            const float f = now == keep ? 1.f : d < 126 ? __fdividef(now, was) * pow2_down(d) : 0.f;  // now <= was 2^d
             s.m[nt][c] = m[nt][c];
             s.iv[nt][c] = now;
             s.l[nt][c] *= pow2_down(d);

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import kv8_ref as ref
-from kv8_forms import FORMS, attend, bf16, check, one_sequence, values
+from kv8_forms import FORMS, attend, bf16, check, i32, one_sequence, values
 
 pytestmark = pytest.mark.gpu
 
@@ -124,4 +124,46 @@ def test_where_one_key_outweighs_the_others(lsa, fmt, form):
         want = torch.from_numpy(p @ hv[j]).to(torch.bfloat16)
         wrong += int((o[i].cpu() != want).sum())
     assert wrong < nq * G * 128 / 100
+    lsa.check_device_error()
+
+
+@pytest.mark.parametrize("tokens", [200, 2048, 64000])   # what the table has room for: CTAs, clusters, pieces
+@pytest.mark.parametrize("fmt,e,new,G", [("e4m3", 30, 24, 4), ("int8", 100, 3, 2), ("e4m3", 118, 9, 8), ("int8", 17, 40, 1)])
+def test_large_values_that_some_queries_do_not_see_yet(lsa, fmt, e, new, G, tokens):
+    """New tokens whose windows begin at different keys: the first keys of a
+    walk are hidden from some of its columns, in pages of large values."""
+    rng = np.random.default_rng(e)
+    n, page = 200, 16
+    v = np.clip(rng.standard_normal((n, 1, 128)) + 0.5, -1.9, 1.9) * 2.0 ** e
+    kv, table = one_sequence(lsa, rng.standard_normal((n, 1, 128)), v, page, fmt)
+    q, hq = bf16(rng.standard_normal((new, G, 128)))
+    wide = np.full((1, -(-tokens // page)), -1, np.int32)
+    wide[:, :table.shape[1]] = table
+    for window in (21, 70):
+        o, lse = lsa.kv8_attn(q, kv, i32(wide), i32([n]), cu=i32([0, new]), window=window)
+        k, w, vs = values(kv, table, fmt, 0)
+        for i in range(new):
+            t = n - new + i
+            j = np.arange(max(0, t - window + 1), t + 1)
+            want, wl, tol, tl = attended(hq[i], k[j], w[j], vs[j], fmt)
+            check(o[i], want, tol)
+            check(lse[i], wl, tl)
+    lsa.check_device_error()
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("first", [True, False])
+def test_values_of_zero_beside_large_ones(lsa, first, form):
+    """Pages of zeros hold all the weight, pages of the largest values none."""
+    rng = np.random.default_rng(95)
+    n, nq, G, page = 512, 16, 4, 32
+    k, v = rng.standard_normal((n, 1, 128)) * 0.5, np.zeros((n, 1, 128))
+    large = (np.arange(n) // page % 4 == 2) if first else (np.arange(n) // page % 4 == 0)
+    v[large] = rng.standard_normal((int(large.sum()), 1, 128)) * 2.0 ** 110
+    k[..., 0] = np.where(large, 30.0, 0.0)[:, None]
+    kv, table = one_sequence(lsa, k, v, page, "e4m3")
+    q = rng.standard_normal((nq, G, 128))
+    q[..., 0] = -100.0                           # 100 * 30 / sqrt(128): 265, or 382 in base 2, below
+    o, lse, _ = attend(lsa, form, bf16(q)[0], kv, table, n)
+    assert not o.any() and torch.isfinite(lse).all()
     lsa.check_device_error()
