@@ -684,7 +684,9 @@ size_t lsa_kv8_sparse_attn_workspace_bytes(const lsa_kv8* kv, int64_t nq, int32_
  * once: made for decoded and drafted tokens, not for whole prompts.
  * Scores are fp32: they and the product of a Q row's and a page's K magnitudes
  * must stay below 2^127.  Elements of Q below 2^-17 of their row's largest are
- * rounded, by at most 2^-25 of it.  Values may be of any magnitude.
+ * rounded, by at most 2^-25 of it.  Values may be of any magnitude; a key whose
+ * score is 126 (base 2) below its row's largest adds nothing, however large its
+ * values are.
  * ws: lsa_kv8_attn_workspace_bytes(), 16-byte aligned; calls that may run at
  * the same time need one each.  hq / hkv must be 1, 2, 4 or 8.
  */
